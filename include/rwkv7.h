@@ -365,6 +365,101 @@ RWKV7_API rwkv7_status rwkv7_wkv_backward_bf16(int B, int T, int H, int N, const
                                                const float *ds_out, float *dr, float *dw, float *dk, float *dv,
                                                float *da, float *db, float *ds_in, rwkv7_stream_t stream);
 
+/* ---- linear attention with one decay per head -----------------------------------------------
+ *
+ * The recurrence above without its low-rank term and with one decay w_h in [0, 1] per head, a constant of
+ * the model (the pages have no counterpart; the state and operand layouts are those of the wkv calls,
+ * so the same buffers serve both):
+ *     S <- w_h S + v_t k_t^T,    y_t = S r_t
+ * r, k, v, y: [B,T,H,64] (prefill), [total_T,H,64] (varlen), [B,H,64] (decode), float32 or bfloat16 bit
+ * patterns; w: float32 [H], device; states float32 [B,H,64,64].  Every w in [0, 1] is exact: 0 (each
+ * token alone) and 1 (no decay) included.  s_in may be NULL (zero) and may equal s_out; ownership,
+ * alignment, status codes and T == 0 as for the wkv calls; B, H <= 65535.
+ *
+ * workspace: caller-owned device memory (16-byte aligned) in which a prefill or backward splits its
+ * sequences into segments that run side by side: rwkv7_linattn_workspace(B, max_T, H) bytes, or
+ * rwkv7_linattn_backward_workspace(B, T, H), are the most it uses (0: it does not split).  With fewer
+ * bytes it splits less, with NULL and 0 not at all; the results are the same up to float32 rounding
+ * order.  The contents need no preparation and mean nothing afterwards; calls that may run at once
+ * need workspaces of their own, replays of a captured call included.
+ *
+ * varlen: cu_seqlens and max_T as for rwkv7_wkv_prefill_varlen_bf16.
+ * backward: gradients of a loss with dL/dy = dy and dL/ds_out = ds_out (NULL: zero).  It needs the
+ *   operands alone, no checkpoints: with G_t = dL/dS_t = dy_t r_t^T + w G_{t+1},
+ *     dr_t = S_t^T dy_t,  dk_t = G_t^T v_t,  dv_t = G_t k_t,  ds_in = w G_0.
+ *   dr, dk, dv [B,T,H,64] are bfloat16 like the operands (each is written once, nothing is
+ *   accumulated in them); ds_in float32 or NULL, and may equal ds_out.  No other output may overlap an
+ *   input.  w gets no gradient. */
+RWKV7_API long long rwkv7_linattn_workspace(int B, int max_T, int H);
+RWKV7_API long long rwkv7_linattn_backward_workspace(int B, int T, int H);
+
+RWKV7_API rwkv7_status rwkv7_linattn_prefill(int B, int T, int H, int N, const float *r, const float *k,
+                                             const float *v, const float *w, const float *s_in, float *y,
+                                             float *s_out, void *workspace, long long workspace_bytes,
+                                             rwkv7_stream_t stream);
+
+RWKV7_API rwkv7_status rwkv7_linattn_prefill_bf16(int B, int T, int H, int N, const uint16_t *r, const uint16_t *k,
+                                                  const uint16_t *v, const float *w, const float *s_in, uint16_t *y,
+                                                  float *s_out, void *workspace, long long workspace_bytes,
+                                                  rwkv7_stream_t stream);
+
+RWKV7_API rwkv7_status rwkv7_linattn_prefill_varlen_bf16(int B, int total_T, int max_T, int H, int N,
+                                                         const int32_t *cu_seqlens, const uint16_t *r,
+                                                         const uint16_t *k, const uint16_t *v, const float *w,
+                                                         const float *s_in, uint16_t *y, float *s_out,
+                                                         void *workspace, long long workspace_bytes,
+                                                         rwkv7_stream_t stream);
+
+RWKV7_API rwkv7_status rwkv7_linattn_decode(int B, int H, int N, const float *r, const float *k, const float *v,
+                                            const float *w, float *s_inout, float *y, rwkv7_stream_t stream);
+
+RWKV7_API rwkv7_status rwkv7_linattn_decode_bf16(int B, int H, int N, const uint16_t *r, const uint16_t *k,
+                                                 const uint16_t *v, const float *w, float *s_inout, uint16_t *y,
+                                                 rwkv7_stream_t stream);
+
+RWKV7_API rwkv7_status rwkv7_linattn_backward_bf16(int B, int T, int H, int N, const uint16_t *r, const uint16_t *k,
+                                                   const uint16_t *v, const float *w, const float *s_in,
+                                                   const uint16_t *dy, const float *ds_out, uint16_t *dr,
+                                                   uint16_t *dk, uint16_t *dv, float *ds_in, void *workspace,
+                                                   long long workspace_bytes, rwkv7_stream_t stream);
+
+/* ---- layer norm over groups, forward and backward ---------------------------------------------
+ *
+ * x [M, G, D]: every one of the M x G vectors of D channels is normalised by its own mean and variance
+ * (divisor D), then scaled and shifted by weight, bias float32 [G, D] (each may be NULL: ones / zeros):
+ *     y = (x - mean) rstd weight + bias,    rstd = 1 / sqrt(var + eps)
+ * G = 1 is the norm over a token's channels (a block's input norms); G = H, D = 64 with eps 64e-5 the
+ * ln_x of the time mix (RWKV-7 G0 7.2B walkthrough, lshu.cn/news/198401, section 7.1), which the wkv
+ * calls apply in their epilogue for inference and which training needs apart, with its gradients.
+ * x, y, dy, dx: float32 or bfloat16 bit patterns, any D >= 1 with G * D <= 2^24 and M * G < 2^31; mean and
+ * rstd float32 [M, G] are what the backward needs (NULL where no backward follows).
+ * backward: with g = dy weight and xh = (x - mean) rstd,
+ *     dx = rstd (g - mean_D(g) - xh mean_D(g xh)),   dweight = sum_M dy xh,   dbias = sum_M dy
+ *   dweight, dbias float32 [G, D], both or neither (NULL: a frozen norm); their sums over the rows are in a fixed
+ *   order, so that repeated calls give the same bits.  They pass through workspace (device, 16-byte
+ *   aligned, rwkv7_layer_norm_workspace bytes at least; its `bf16` says the type of x; not needed for a frozen
+ *   norm).  No output may overlap an input.  Every pointer 16-byte aligned; M == 0 writes zeros to
+ *   dweight and dbias and nothing else.  Status codes as for the other calls. */
+RWKV7_API long long rwkv7_layer_norm_workspace(int bf16, int M, int G, int D);
+
+RWKV7_API rwkv7_status rwkv7_layer_norm(int M, int G, int D, float eps, const float *x, const float *weight,
+                                        const float *bias, float *y, float *mean, float *rstd,
+                                        rwkv7_stream_t stream);
+
+RWKV7_API rwkv7_status rwkv7_layer_norm_bf16(int M, int G, int D, float eps, const uint16_t *x, const float *weight,
+                                             const float *bias, uint16_t *y, float *mean, float *rstd,
+                                             rwkv7_stream_t stream);
+
+RWKV7_API rwkv7_status rwkv7_layer_norm_backward(int M, int G, int D, const float *dy, const float *x,
+                                                 const float *weight, const float *mean, const float *rstd,
+                                                 float *dx, float *dweight, float *dbias, void *workspace,
+                                                 long long workspace_bytes, rwkv7_stream_t stream);
+
+RWKV7_API rwkv7_status rwkv7_layer_norm_backward_bf16(int M, int G, int D, const uint16_t *dy, const uint16_t *x,
+                                                      const float *weight, const float *mean, const float *rstd,
+                                                      uint16_t *dx, float *dweight, float *dbias, void *workspace,
+                                                      long long workspace_bytes, rwkv7_stream_t stream);
+
 /* ---- test hook ------------------------------------------------------------------------------
  *
  * For tests of the failure path only (the pages have no counterpart): sets, for every later launch

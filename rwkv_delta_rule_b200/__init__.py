@@ -15,6 +15,7 @@ per batch row b and head h, with a float32 64 x 64 state S:
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -32,6 +33,11 @@ __all__ = [
     "rwkv7_wkv_decode_ext_bf16state",
     "rwkv7_wkv_prefill_host_bf16", "rwkv7_wkv_prefill_host_noalloc_bf16", "NOALLOC_STAGING_BYTES", "prefill", "decode_", "prefill_model_native", "decode_model_native_", "prefill_ext", "decode_ext_",
     "prefill_save", "backward", "EXPORTED_SYMBOLS",
+    "rwkv7_linattn_workspace", "rwkv7_linattn_backward_workspace", "rwkv7_linattn_prefill", "rwkv7_linattn_prefill_bf16",
+    "rwkv7_linattn_prefill_varlen_bf16", "rwkv7_linattn_decode", "rwkv7_linattn_decode_bf16",
+    "rwkv7_linattn_backward_bf16", "rwkv7_layer_norm_workspace", "rwkv7_layer_norm", "rwkv7_layer_norm_bf16",
+    "rwkv7_layer_norm_backward", "rwkv7_layer_norm_backward_bf16", "linattn_prefill", "linattn_prefill_varlen",
+    "linattn_decode_", "linattn_backward", "layer_norm", "layer_norm_backward",
 ]
 
 RWKV7_PATH_AUTO, RWKV7_PATH_SCAN, RWKV7_PATH_CHUNK = 0, 1, 2
@@ -46,6 +52,10 @@ EXPORTED_SYMBOLS = (
     "rwkv7_wkv_prefill_save_bf16", "rwkv7_wkv_backward_bf16", "rwkv7_wkv_decode_bf16_bf16state",
     "rwkv7_wkv_prefill_host_bf16", "rwkv7_status_string", "rwkv7_get_last_error", "rwkv7_version",
     "rwkv7_wkv_prefill_host_noalloc_bf16", "rwkv7_test_set_wait_hooks", "rwkv7_wkv_decode_ext_bf16state",
+    "rwkv7_linattn_workspace", "rwkv7_linattn_backward_workspace", "rwkv7_linattn_prefill", "rwkv7_linattn_prefill_bf16",
+    "rwkv7_linattn_prefill_varlen_bf16", "rwkv7_linattn_decode", "rwkv7_linattn_decode_bf16",
+    "rwkv7_linattn_backward_bf16", "rwkv7_layer_norm_workspace", "rwkv7_layer_norm", "rwkv7_layer_norm_bf16",
+    "rwkv7_layer_norm_backward", "rwkv7_layer_norm_backward_bf16",
 )
 # RWKV7_NOALLOC_STAGING_BYTES of include/rwkv7.h: the staging limit of rwkv7_wkv_prefill_host_noalloc_bf16
 NOALLOC_STAGING_BYTES = 32 * 1024 * 1024
@@ -81,7 +91,7 @@ def load_library() -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError(f"librwkv7.so not built ({path}); run `python -m rwkv_delta_rule_b200.build`")
     lib = ctypes.CDLL(path)
-    vp, ci = ctypes.c_void_p, ctypes.c_int
+    vp, ci, cl = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
     pre = [ci, ci, ci, ci] + [vp] * 6 + [vp, vp, vp, vp]
     for name, args in (
         ("rwkv7_wkv_prefill", pre),
@@ -101,10 +111,25 @@ def load_library() -> ctypes.CDLL:
         ("rwkv7_wkv_prefill_host_bf16", [ci, ci, ci, ci, ci] + [vp] * 6 + [vp, vp, vp] + [vp] * 6 + [vp, vp, vp]
          + [ci, vp]),
         ("rwkv7_wkv_prefill_host_noalloc_bf16", [ci] + pre),
+        ("rwkv7_linattn_prefill", [ci] * 4 + [vp] * 7 + [vp, cl, vp]),
+        ("rwkv7_linattn_prefill_bf16", [ci] * 4 + [vp] * 7 + [vp, cl, vp]),
+        ("rwkv7_linattn_prefill_varlen_bf16", [ci] * 5 + [vp] * 8 + [vp, cl, vp]),
+        ("rwkv7_linattn_decode", [ci] * 3 + [vp] * 7),
+        ("rwkv7_linattn_decode_bf16", [ci] * 3 + [vp] * 7),
+        ("rwkv7_linattn_backward_bf16", [ci] * 4 + [vp] * 11 + [vp, cl, vp]),
+        ("rwkv7_layer_norm", [ci] * 3 + [ctypes.c_float] + [vp] * 7),
+        ("rwkv7_layer_norm_bf16", [ci] * 3 + [ctypes.c_float] + [vp] * 7),
+        ("rwkv7_layer_norm_backward", [ci] * 3 + [vp] * 8 + [vp, cl, vp]),
+        ("rwkv7_layer_norm_backward_bf16", [ci] * 3 + [vp] * 8 + [vp, cl, vp]),
     ):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ci
+    for name, n in (("rwkv7_linattn_workspace", 3), ("rwkv7_linattn_backward_workspace", 3),
+                    ("rwkv7_layer_norm_workspace", 4)):
+        fn = getattr(lib, name)
+        fn.argtypes = [ci] * n
+        fn.restype = cl
     lib.rwkv7_status_string.argtypes = [ci]
     lib.rwkv7_status_string.restype = ctypes.c_char_p
     lib.rwkv7_get_last_error.argtypes = []
@@ -383,6 +408,210 @@ def rwkv7_wkv_backward_bf16(r, w, k, v, a, b, states, dy, ds_out, dr, dw, dk, dv
           *[_ptr(t) for t in (dr, dw, dk, dv, da, db, ds_in)], _stream(stream))
 
 
+# ---- linear attention with one decay per head, and the layer norm --------------------------------------
+
+class _Where:
+    """The device and stream of a call: its tensors lie on one device, which need not be the current one."""
+
+    def __init__(self, stream, first, *rest):
+        for t in (first,) + rest:
+            if t is not None and t.device != first.device:
+                raise ValueError(f"tensors on {first.device} and {t.device}: one device is wanted")
+        self.device = first.device
+        if stream is None:
+            stream = torch.cuda.current_stream(first.device)
+        elif isinstance(stream, torch.cuda.Stream) and stream.device != first.device:
+            raise ValueError(f"a stream of {stream.device} for tensors on {first.device}")
+        self.stream = _stream(stream)
+
+    def call(self, name, *args):
+        if torch.cuda.current_device() == self.device.index:
+            _call(name, *args, self.stream)
+        else:
+            with torch.cuda.device(self.device):
+                _call(name, *args, self.stream)
+
+
+def _on(stream, device):
+    """Where a convenience allocates: on the stream that its kernels run on, so that nothing it frees
+    is handed out again before they are done."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _workspace(n: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(n, dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def _check_workspace(ws) -> int:
+    if ws is None:
+        return 0
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return ws.numel() * ws.element_size()
+
+
+def rwkv7_linattn_workspace(B: int, max_T: int, H: int) -> int:
+    """Bytes of workspace that a linear-attention prefill of this size uses at most."""
+    return int(load_library().rwkv7_linattn_workspace(int(B), int(max_T), int(H)))
+
+
+def rwkv7_linattn_backward_workspace(B: int, T: int, H: int) -> int:
+    """Bytes of workspace that ``rwkv7_linattn_backward_bf16`` uses at most."""
+    return int(load_library().rwkv7_linattn_backward_workspace(int(B), int(T), int(H)))
+
+
+def _linattn_prefill(name, dtype, r, k, v, w, s_in, y, s_out, workspace, stream):
+    _check(r, "r", dtype)
+    if r.dim() != 4:
+        raise ValueError(f"r must be [B, T, H, 64], got {tuple(r.shape)}")
+    B, T, H, N = r.shape
+    for nm, t in (("k", k), ("v", v), ("y", y)):
+        _check(t, nm, dtype, (B, T, H, N))
+    _check(w, "w", torch.float32, (H,))
+    _check(s_in, "s_in", torch.float32, (B, H, N, N), allow_none=True)
+    _check(s_out, "s_out", torch.float32, (B, H, N, N))
+    nb = _check_workspace(workspace)
+    _Where(stream, r, k, v, w, s_in, y, s_out, workspace).call(
+        name, B, T, H, N, *[_ptr(t) for t in (r, k, v, w, s_in, y, s_out, workspace)], nb)
+
+
+def rwkv7_linattn_prefill(r, k, v, w, s_in, y, s_out, workspace=None, stream=None) -> None:
+    """float32 prefill of ``S <- w S + v k^T, y = S r``: operands / y ``[B,T,H,64]``, w float32 ``[H]``, states
+    ``[B,H,64,64]`` (s_in may be None, or s_out)."""
+    _linattn_prefill("rwkv7_linattn_prefill", torch.float32, r, k, v, w, s_in, y, s_out, workspace, stream)
+
+
+def rwkv7_linattn_prefill_bf16(r, k, v, w, s_in, y, s_out, workspace=None, stream=None) -> None:
+    """``rwkv7_linattn_prefill`` on bfloat16 operands and y (states and w float32)."""
+    _linattn_prefill("rwkv7_linattn_prefill_bf16", torch.bfloat16, r, k, v, w, s_in, y, s_out, workspace, stream)
+
+
+def rwkv7_linattn_prefill_varlen_bf16(cu_seqlens, max_T, r, k, v, w, s_in, y, s_out, workspace=None,
+                                      stream=None) -> None:
+    """Ragged bfloat16 prefill: operands / y ``[total_T,H,64]`` packed, ``cu_seqlens`` int32 ``[B+1]`` on the device."""
+    _check(r, "r", torch.bfloat16)
+    if r.dim() != 3:
+        raise ValueError(f"r must be [total_T, H, 64], got {tuple(r.shape)}")
+    total, H, N = r.shape
+    Bn = cu_seqlens.numel() - 1
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (Bn + 1,))
+    for nm, t in (("k", k), ("v", v), ("y", y)):
+        _check(t, nm, torch.bfloat16, (total, H, N))
+    _check(w, "w", torch.float32, (H,))
+    _check(s_in, "s_in", torch.float32, (Bn, H, N, N), allow_none=True)
+    _check(s_out, "s_out", torch.float32, (Bn, H, N, N))
+    nb = _check_workspace(workspace)
+    _Where(stream, r, k, v, w, s_in, y, s_out, cu_seqlens, workspace).call(
+        "rwkv7_linattn_prefill_varlen_bf16", Bn, total, int(max_T), H, N,
+        *[_ptr(t) for t in (cu_seqlens, r, k, v, w, s_in, y, s_out, workspace)], nb)
+
+
+def _linattn_decode(name, dtype, r, k, v, w, s_inout, y, stream):
+    _check(r, "r", dtype)
+    if r.dim() != 3:
+        raise ValueError(f"r must be [B, H, 64], got {tuple(r.shape)}")
+    B, H, N = r.shape
+    for nm, t in (("k", k), ("v", v), ("y", y)):
+        _check(t, nm, dtype, (B, H, N))
+    _check(w, "w", torch.float32, (H,))
+    _check(s_inout, "s_inout", torch.float32, (B, H, N, N))
+    _Where(stream, r, k, v, w, s_inout, y).call(name, B, H, N, *[_ptr(t) for t in (r, k, v, w, s_inout, y)])
+
+
+def rwkv7_linattn_decode(r, k, v, w, s_inout, y, stream=None) -> None:
+    """float32 one-token step: operands / y ``[B,H,64]``, state ``[B,H,64,64]`` updated in place."""
+    _linattn_decode("rwkv7_linattn_decode", torch.float32, r, k, v, w, s_inout, y, stream)
+
+
+def rwkv7_linattn_decode_bf16(r, k, v, w, s_inout, y, stream=None) -> None:
+    """bfloat16 one-token step, float32 state updated in place."""
+    _linattn_decode("rwkv7_linattn_decode_bf16", torch.bfloat16, r, k, v, w, s_inout, y, stream)
+
+
+def rwkv7_linattn_backward_bf16(r, k, v, w, s_in, dy, ds_out, dr, dk, dv, ds_in, workspace=None, stream=None) -> None:
+    """Gradients of a loss with dL/dy = ``dy`` (bf16) and dL/ds_out = ``ds_out`` (float32 or None) with respect
+    to r, k, v (bf16 ``[B,T,H,64]``) and s_in (``ds_in`` float32 or None)."""
+    _check(r, "r", torch.bfloat16)
+    if r.dim() != 4:
+        raise ValueError(f"r must be [B, T, H, 64], got {tuple(r.shape)}")
+    B, T, H, N = r.shape
+    for nm, t in (("k", k), ("v", v), ("dy", dy), ("dr", dr), ("dk", dk), ("dv", dv)):
+        _check(t, nm, torch.bfloat16, (B, T, H, N))
+    _check(w, "w", torch.float32, (H,))
+    for nm, t in (("s_in", s_in), ("ds_out", ds_out), ("ds_in", ds_in)):
+        _check(t, nm, torch.float32, (B, H, N, N), allow_none=True)
+    nb = _check_workspace(workspace)
+    ts = (r, k, v, w, s_in, dy, ds_out, dr, dk, dv, ds_in, workspace)
+    _Where(stream, *ts).call("rwkv7_linattn_backward_bf16", B, T, H, N, *[_ptr(t) for t in ts], nb)
+
+
+def rwkv7_layer_norm_workspace(bf16: bool, M: int, G: int, D: int) -> int:
+    """Bytes of workspace that the layer norm's backward needs for x ``[M, G, D]``."""
+    return int(load_library().rwkv7_layer_norm_workspace(int(bool(bf16)), int(M), int(G), int(D)))
+
+
+def _norm_shape(x, name):
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [M, G, D], got {tuple(x.shape)}")
+    return x.shape
+
+
+def _layer_norm(name, dtype, x, weight, bias, eps, y, mean, rstd, stream):
+    _check(x, "x", dtype)
+    M, G, D = _norm_shape(x, "x")
+    _check(y, "y", dtype, (M, G, D))
+    for nm, t in (("weight", weight), ("bias", bias)):
+        _check(t, nm, torch.float32, (G, D), allow_none=True)
+    for nm, t in (("mean", mean), ("rstd", rstd)):
+        _check(t, nm, torch.float32, (M, G), allow_none=True)
+    _Where(stream, x, weight, bias, y, mean, rstd).call(name, M, G, D, float(eps),
+                                                        *[_ptr(t) for t in (x, weight, bias, y, mean, rstd)])
+
+
+def rwkv7_layer_norm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None) -> None:
+    """float32 layer norm of x ``[M,G,D]`` over D; weight, bias float32 ``[G,D]`` or None; mean, rstd float32
+    ``[M,G]`` (for the backward) or None."""
+    _layer_norm("rwkv7_layer_norm", torch.float32, x, weight, bias, eps, y, mean, rstd, stream)
+
+
+def rwkv7_layer_norm_bf16(x, weight, bias, eps, y, mean=None, rstd=None, stream=None) -> None:
+    """``rwkv7_layer_norm`` on bfloat16 x and y."""
+    _layer_norm("rwkv7_layer_norm_bf16", torch.bfloat16, x, weight, bias, eps, y, mean, rstd, stream)
+
+
+def _layer_norm_backward(name, dtype, dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, stream):
+    _check(x, "x", dtype)
+    M, G, D = _norm_shape(x, "x")
+    for nm, t in (("dy", dy), ("dx", dx)):
+        _check(t, nm, dtype, (M, G, D))
+    for nm, t in (("weight", weight), ("dweight", dweight), ("dbias", dbias)):
+        _check(t, nm, torch.float32, (G, D), allow_none=True)
+    for nm, t in (("mean", mean), ("rstd", rstd)):
+        _check(t, nm, torch.float32, (M, G))
+    nb = _check_workspace(workspace)
+    ts = (dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
+    _Where(stream, *ts).call(name, M, G, D, *[_ptr(t) for t in ts], nb)
+
+
+def rwkv7_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, workspace=None,
+                              stream=None) -> None:
+    """Gradients of ``rwkv7_layer_norm``: dx, and dweight and dbias float32 ``[G,D]`` (both or neither; they need a
+    workspace of ``rwkv7_layer_norm_workspace`` bytes)."""
+    _layer_norm_backward("rwkv7_layer_norm_backward", torch.float32, dy, x, weight, mean, rstd, dx, dweight, dbias,
+                         workspace, stream)
+
+
+def rwkv7_layer_norm_backward_bf16(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, workspace=None,
+                                   stream=None) -> None:
+    """``rwkv7_layer_norm_backward`` on bfloat16 dy, x and dx."""
+    _layer_norm_backward("rwkv7_layer_norm_backward_bf16", torch.bfloat16, dy, x, weight, mean, rstd, dx, dweight,
+                         dbias, workspace, stream)
+
+
 def rwkv7_status_string(status: int) -> str:
     return load_library().rwkv7_status_string(int(status)).decode()
 
@@ -484,3 +713,96 @@ def backward(r, w, k, v, a, b, states, dy, ds_out=None, *, stream=None):
     ds_in = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
     rwkv7_wkv_backward_bf16(r, w, k, v, a, b, states, dy, ds_out, *g, ds_in, stream=stream)
     return tuple(g) + (ds_in,)
+
+
+def linattn_prefill(r, k, v, w, s_in=None, *, stream=None):
+    """Allocate ``y`` and ``s_out`` and run the linear-attention prefill; returns ``(y, s_out)``."""
+    B, T, H, N = r.shape
+    with _on(stream, r.device):
+        y = torch.empty_like(r)
+        s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
+        ws = _workspace(rwkv7_linattn_workspace(B, T, H), r.device)
+    f = rwkv7_linattn_prefill if r.dtype == torch.float32 else rwkv7_linattn_prefill_bf16
+    f(r, k, v, w, s_in, y, s_out, ws, stream)
+    return y, s_out
+
+
+def linattn_prefill_varlen(cu_seqlens, max_T, r, k, v, w, s_in=None, *, stream=None):
+    """Allocate ``y`` and ``s_out`` and run the ragged linear-attention prefill; returns ``(y, s_out)``.
+    Tokens of ``y`` that no row owns are left unset."""
+    total, H, N = r.shape
+    B = cu_seqlens.numel() - 1
+    with _on(stream, r.device):
+        y = torch.empty_like(r)
+        s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
+        ws = _workspace(rwkv7_linattn_workspace(B, max_T, H), r.device)
+    rwkv7_linattn_prefill_varlen_bf16(cu_seqlens, max_T, r, k, v, w, s_in, y, s_out, ws, stream)
+    return y, s_out
+
+
+def linattn_decode_(r, k, v, w, state, y=None, *, stream=None):
+    """One linear-attention step updating ``state`` in place; returns ``y``."""
+    if y is None:
+        with _on(stream, r.device):
+            y = torch.empty_like(r)
+    f = rwkv7_linattn_decode if r.dtype == torch.float32 else rwkv7_linattn_decode_bf16
+    f(r, k, v, w, state, y, stream)
+    return y
+
+
+def linattn_backward(r, k, v, w, dy, s_in=None, ds_out=None, *, stream=None):
+    """Allocate and run the linear-attention backward; returns ``(dr, dk, dv, ds_in)`` (bf16, ds_in float32)."""
+    B, T, H, N = r.shape
+    with _on(stream, r.device):
+        dr, dk, dv = (torch.empty_like(r) for _ in range(3))
+        ds_in = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
+        ws = _workspace(rwkv7_linattn_backward_workspace(B, T, H), r.device)
+    rwkv7_linattn_backward_bf16(r, k, v, w, s_in, dy, ds_out, dr, dk, dv, ds_in, ws, stream)
+    return dr, dk, dv, ds_in
+
+
+def _norm_view(x, weight, bias, group):
+    """x as [M, G, D]: the channels normalised together are the last dimension, and weight and bias, of
+    shape [D] or [G, D], say whether the dimension before it numbers groups (``group`` where both are None)."""
+    p = weight if weight is not None else bias
+    grouped = p.dim() == 2 if p is not None else group
+    if x.dim() < (2 if grouped else 1):
+        raise ValueError(f"x must have a last dimension of channels, got {tuple(x.shape)}")
+    G, D = (x.shape[-2] if grouped else 1), x.shape[-1]
+    M = x.numel() // (G * D) if G * D else 0
+    return (M, G, D), x.shape[:-1], tuple(x.shape[-2:] if grouped else x.shape[-1:])
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, *, grouped=False, stream=None):
+    """Layer norm over the last dimension; returns ``(y, mean, rstd)`` (mean, rstd float32, of x's shape without
+    its last dimension).  weight, bias: float32 ``[D]``, or ``[G, D]`` for x ``[..., G, D]`` with a scale for
+    each group; ``grouped`` says which where both are None."""
+    (M, G, D), lead, p = _norm_view(x, weight, bias, grouped)
+    for nm, t in (("weight", weight), ("bias", bias)):
+        _check(t, nm, torch.float32, p, allow_none=True)
+    _check(x, "x", x.dtype)
+    with _on(stream, x.device):
+        y = torch.empty_like(x)
+        mean, rstd = (torch.empty(lead, dtype=torch.float32, device=x.device) for _ in range(2))
+    f = rwkv7_layer_norm if x.dtype == torch.float32 else rwkv7_layer_norm_bf16
+    f(x.view(M, G, D), None if weight is None else weight.view(G, D), None if bias is None else bias.view(G, D), eps,
+      y.view(M, G, D), mean.view(M, G), rstd.view(M, G), stream)
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, *, grouped=False, stream=None):
+    """Gradients of ``layer_norm``; returns ``(dx, dweight, dbias)`` (dweight, dbias float32 of weight's shape)."""
+    (M, G, D), lead, p = _norm_view(x, weight, None, grouped)
+    _check(weight, "weight", torch.float32, p, allow_none=True)
+    _check(x, "x", x.dtype)
+    _check(dy, "dy", x.dtype, x.shape)
+    for nm, t in (("mean", mean), ("rstd", rstd)):
+        _check(t, nm, torch.float32, lead)
+    with _on(stream, x.device):
+        dx = torch.empty_like(x)
+        dweight, dbias = (torch.empty(p, dtype=torch.float32, device=x.device) for _ in range(2))
+        ws = _workspace(rwkv7_layer_norm_workspace(x.dtype == torch.bfloat16, M, G, D), x.device)
+    f = rwkv7_layer_norm_backward if x.dtype == torch.float32 else rwkv7_layer_norm_backward_bf16
+    f(dy.view(M, G, D), x.view(M, G, D), None if weight is None else weight.view(G, D), mean.view(M, G),
+      rstd.view(M, G), dx.view(M, G, D), dweight.view(G, D), dbias.view(G, D), ws, stream)
+    return dx, dweight, dbias

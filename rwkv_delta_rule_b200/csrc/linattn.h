@@ -1,0 +1,84 @@
+// linattn.h -- what the kernels of the head-decay linear attention share: arguments, segments of a
+// sequence, powers of a decay.  Internal, not exported.
+#pragma once
+
+#include "common.cuh"
+
+namespace rwkv7 {
+namespace lin {
+
+// One pass of the recurrence over [B, T, H, 64] (or packed ragged) operands, for every (b, h):
+//   forward  S <- w S + v k^T;  out = S q          reverse (tokens from the last)  S <- S + v k^T;  out = S q;  S <- w S
+// Rows of S are the channels of v, columns those of k.
+template <typename TIn> struct Pass {
+  const TIn *q, *k, *v;
+  TIn *out;
+  const float *s_in;     // [B, H, 64, 64] or nullptr (zero)
+  float *s_out;          // [B, H, 64, 64] or nullptr
+  int s_in_t, s_out_t;   // the state is stored transposed there
+  float *ws;             // nseg > 1: [B, H, nseg, 64, 64], slot z is the state that segment z begins with
+  int reverse;
+  int state_only;        // no outputs: what each segment adds to the state, for the segment after it (q, out unused)
+};
+
+struct Shape {
+  const float *w;  // [H]
+  const int32_t *cu_seqlens;  // nullptr: fixed length T
+  int T;
+  long long total_T;
+  int H;
+  int nseg;     // segments per sequence (1: the whole sequence)
+  int seg_len;  // tokens per segment, a multiple of 128; the last segment runs to the sequence's end
+};
+
+// Tokens lo .. lo + len - 1 of the packed operands; `first` / `last`: this segment begins / ends the
+// sequence.  len = -1: nothing to do.
+struct Segment {
+  long long lo;
+  int len;
+  bool first, last;
+};
+__device__ __forceinline__ Segment segment(const Shape &P, int b, int z) {
+  const SeqBounds sb = seq_bounds(P.cu_seqlens, b, P.T, P.total_T);
+  Segment s{0, -1, z == 0, false};
+  if (sb.len < 0) return s;
+  const long long off = static_cast<long long>(z) * P.seg_len;
+  if (z > 0 && off >= sb.len) return s;
+  const long long left = sb.len - off;
+  s.lo = sb.start + off;
+  s.last = z == P.nseg - 1 || left <= P.seg_len;
+  s.len = static_cast<int>(s.last ? left : P.seg_len);
+  return s;
+}
+
+// w^n in float64 by squaring (w^0 = 1 for every w, zero included); one rounding per product, so far
+// below float32's step for every n here.
+__device__ __forceinline__ double powi(double w, long long n) {
+  double r = 1.0, p = w;
+  for (; n > 0; n >>= 1) {
+    if (n & 1) r *= p;
+    p *= p;
+  }
+  return r;
+}
+
+// element (row, col) of a state as it is stored
+__device__ __forceinline__ int state_at(int transposed, int row, int col) {
+  return transposed ? col * kN + row : row * kN + col;
+}
+
+}  // namespace lin
+
+// Launchers of the passes; TIn: float or uint16_t (bfloat16 bits).
+template <typename TIn>
+cudaError_t launch_linattn_scan(const lin::Pass<TIn> &pass, const lin::Shape &shape, int B, cudaStream_t stream);
+// A pass with state_only leaves what each segment adds to the state in the slot of the segment
+// after it.  This turns the slots into the states that the segments begin with; the segments read
+// only those, so s_in may be s_out.
+template <typename TIn>
+cudaError_t launch_linattn_join(const lin::Pass<TIn> &pass, const lin::Shape &shape, int B, cudaStream_t stream);
+template <typename TIn>
+cudaError_t launch_linattn_decode(const TIn *r, const TIn *k, const TIn *v, const float *w, float *s, TIn *y, int B,
+                                  int H, cudaStream_t stream);
+
+}  // namespace rwkv7

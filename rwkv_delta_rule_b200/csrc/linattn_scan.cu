@@ -1,0 +1,202 @@
+// linattn_scan.cu -- linear attention with one decay per head, token by token with the float32 state
+// in registers:  S <- w S + v k^T,  y = S q,  and the same walked from the last token for gradients.
+//
+// One CTA of 128 threads holds a (b, h) pair's 64 x 64 state: thread (rs, q) has rows 4 rs .. 4 rs + 3
+// and columns 4 q .. 4 q + 3, 32 + 4 q .. 32 + 4 q + 3.  The chain through the state is one
+// multiply-add per token, so the walk is bound by its 96 float32 operations and 5 shared-memory loads
+// per thread and token, not by latency.  The read-out's row sums meet in a 4-shuffle reduce-scatter
+// over the 8 lanes of a row group.  Operands are staged by cp.async in double-buffered tiles.
+#include "linattn.h"
+
+namespace rwkv7 {
+namespace lin {
+
+constexpr int kThreads = 128;
+template <typename TIn> struct Tile {
+  static constexpr int kTok = sizeof(TIn) == 2 ? 32 : 16;     // tokens per tile
+  static constexpr int kEPC = 16 / static_cast<int>(sizeof(TIn));
+  static constexpr int kElems = kTok * 3 * kN;                // q, k, v
+  static constexpr size_t kSmem = 2 * kElems * sizeof(TIn) + kTok * kN * sizeof(float);
+};
+
+template <typename TIn, bool kOut>
+__device__ __forceinline__ void stage(const Pass<TIn> &A, TIn *buf, long long tok0, int ntok, int H, int h) {
+  using C = Tile<TIn>;
+  constexpr int kPer = kN / C::kEPC;  // 16-byte pieces of a vector
+  for (int c = threadIdx.x; c < ntok * 3 * kPer; c += kThreads) {
+    const int tt = c / (3 * kPer), rem = c - tt * (3 * kPer), vid = rem / kPer, part = rem - vid * kPer;
+    if (!kOut && vid == 0) continue;
+    const TIn *src = vid == 0 ? A.q : vid == 1 ? A.k : A.v;
+    cp_async16(buf + (tt * 3 + vid) * kN + part * C::kEPC, src + ((tok0 + tt) * H + h) * kN + part * C::kEPC);
+  }
+}
+
+template <typename TIn, bool kRev, bool kOut>
+__global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const Pass<TIn> A, const Shape P) {
+  using C = Tile<TIn>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  TIn *bufs = reinterpret_cast<TIn *>(smem_raw);
+  float *ys = reinterpret_cast<float *>(smem_raw + 2 * C::kElems * sizeof(TIn));
+  const int h = blockIdx.x, b = blockIdx.y;
+  // the state pass covers the segments that another one continues from
+  const int z = blockIdx.z + (!kOut && kRev ? 1 : 0);
+  pdl_wait();
+  const Segment sg = segment(P, b, z);
+  if (sg.len < 0) return;
+  if (!kOut && (kRev ? sg.first : sg.last)) return;
+  const long long pair = static_cast<long long>(b) * P.H + h;
+  const int tid = threadIdx.x, q = tid & 7, row0 = 4 * (tid >> 3);
+  const float w = P.w[h];
+
+  float s[4][8];
+  const float *from = !kOut ? nullptr : P.nseg > 1 ? A.ws + (pair * P.nseg + z) * (kN * kN) : A.s_in + pair * (kN * kN);
+  const int from_t = P.nseg == 1 && A.s_in_t;
+  if (P.nseg == 1 && A.s_in == nullptr) from = nullptr;
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int col = (e >> 2) * 32 + 4 * q + (e & 3);
+      s[m][e] = from == nullptr ? 0.f : from[state_at(from_t, row0 + m, col)];
+    }
+
+  const int ntiles = (sg.len + C::kTok - 1) / C::kTok;
+  auto tile_tok = [&](int i) { return (kRev ? ntiles - 1 - i : i) * C::kTok; };
+  if (ntiles > 0) {
+    const int t0 = tile_tok(0);
+    stage<TIn, kOut>(A, bufs, sg.lo + t0, min(C::kTok, sg.len - t0), P.H, h);
+    cp_async_commit();
+  }
+  for (int i = 0; i < ntiles; ++i) {
+    const int t0 = tile_tok(i), ntok = min(C::kTok, sg.len - t0);
+    if (i + 1 < ntiles) {
+      const int t1 = tile_tok(i + 1);
+      stage<TIn, kOut>(A, bufs + ((i + 1) & 1) * C::kElems, sg.lo + t1, min(C::kTok, sg.len - t1), P.H, h);
+      cp_async_commit();
+      cp_async_wait<1>();
+    } else {
+      cp_async_wait<0>();
+    }
+    __syncthreads();
+    const TIn *buf = bufs + (i & 1) * C::kElems;
+#pragma unroll 2
+    for (int u = 0; u < ntok; ++u) {
+      const int tt = kRev ? ntok - 1 - u : u;
+      const TIn *tk = buf + tt * 3 * kN;
+      float kk[8], vv[4], p[4];
+      Elem<TIn>::load4(tk + kN + 4 * q, kk);
+      Elem<TIn>::load4(tk + kN + 32 + 4 * q, kk + 4);
+      Elem<TIn>::load4(tk + 2 * kN + row0, vv);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[m][e] = kRev ? fmaf(vv[m], kk[e], s[m][e]) : fmaf(s[m][e], w, vv[m] * kk[e]);
+      if (kOut) {
+        float qq[8];
+        Elem<TIn>::load4(tk + 4 * q, qq);
+        Elem<TIn>::load4(tk + 32 + 4 * q, qq + 4);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          float x = s[m][0] * qq[0], y = s[m][1] * qq[1];
+#pragma unroll
+          for (int e = 2; e < 8; e += 2) {
+            x = fmaf(s[m][e], qq[e], x);
+            y = fmaf(s[m][e + 1], qq[e + 1], y);
+          }
+          p[m] = x + y;
+        }
+        const bool h4 = (q & 4) != 0, h2 = (q & 2) != 0;
+        const float a0 = (h4 ? p[2] : p[0]) + __shfl_xor_sync(0xffffffffu, h4 ? p[0] : p[2], 4);
+        const float a1 = (h4 ? p[3] : p[1]) + __shfl_xor_sync(0xffffffffu, h4 ? p[1] : p[3], 4);
+        float y = (h2 ? a1 : a0) + __shfl_xor_sync(0xffffffffu, h2 ? a0 : a1, 2);
+        y += __shfl_xor_sync(0xffffffffu, y, 1);
+        if ((q & 1) == 0) ys[tt * kN + row0 + (h4 ? 2 : 0) + (h2 ? 1 : 0)] = y;
+      }
+      if (kRev) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[m][e] *= w;
+      }
+    }
+    __syncthreads();
+    if (kOut) {
+      for (int e = tid; e < ntok * kN; e += kThreads)
+        Elem<TIn>::store(A.out + ((sg.lo + t0 + (e >> 6)) * P.H + h) * kN + (e & 63), ys[e]);
+      // the next tile writes ys only behind the barrier after its loads
+    }
+  }
+
+  const bool ends = kRev ? sg.first : sg.last;
+  float *to = !kOut ? A.ws + (pair * P.nseg + (kRev ? z - 1 : z + 1)) * (kN * kN) : A.s_out + pair * (kN * kN);
+  if (!kOut || (ends && A.s_out != nullptr)) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int col = (e >> 2) * 32 + 4 * q + (e & 3);
+        to[state_at(kOut && A.s_out_t, row0 + m, col)] = s[m][e];
+      }
+  }
+}
+
+// One thread per 4 columns of a state row, along the segments.
+template <typename TIn> __global__ void __launch_bounds__(256) linattn_join_kernel(const Pass<TIn> A, const Shape P) {
+  const int h = blockIdx.x, b = blockIdx.y;
+  pdl_wait();
+  const SeqBounds sb = seq_bounds(P.cu_seqlens, b, P.T, P.total_T);
+  if (sb.len < 0) return;
+  const long long segs = (static_cast<long long>(sb.len) + P.seg_len - 1) / P.seg_len;
+  const int n = static_cast<int>(segs < 1 ? 1 : segs < P.nseg ? segs : P.nseg);
+  const long long pair = static_cast<long long>(b) * P.H + h;
+  const int e4 = blockIdx.z * 256 + threadIdx.x, row = e4 >> 4, col = 4 * (e4 & 15);
+  const double w = P.w[h];
+  const float wl = static_cast<float>(powi(w, P.seg_len));
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (A.s_in != nullptr) {
+    const float *f = A.s_in + pair * (kN * kN);
+    s = make_float4(f[state_at(A.s_in_t, row, col)], f[state_at(A.s_in_t, row, col + 1)],
+                    f[state_at(A.s_in_t, row, col + 2)], f[state_at(A.s_in_t, row, col + 3)]);
+  }
+  float *ws = A.ws + pair * P.nseg * (kN * kN) + row * kN + col;
+  for (int i = 0; i < n; ++i) {
+    float4 *p = reinterpret_cast<float4 *>(ws + static_cast<long long>(A.reverse ? n - 1 - i : i) * (kN * kN));
+    if (i > 0) {
+      // the decay over the segment before; the sequence's last one may be of another length
+      float f = wl;
+      if (A.reverse && i == 1) f = static_cast<float>(powi(w, sb.len - static_cast<long long>(n - 1) * P.seg_len));
+      const float4 u = *p;
+      s = make_float4(fmaf(s.x, f, u.x), fmaf(s.y, f, u.y), fmaf(s.z, f, u.z), fmaf(s.w, f, u.w));
+    }
+    *p = s;
+  }
+}
+
+}  // namespace lin
+
+template <typename TIn>
+cudaError_t launch_linattn_scan(const lin::Pass<TIn> &A, const lin::Shape &P, int B, cudaStream_t stream) {
+  using namespace lin;
+  auto run = [&](auto kern, int nz) -> cudaError_t {
+    if (nz <= 0) return cudaSuccess;
+    kern<<<dim3(P.H, B, nz), kThreads, Tile<TIn>::kSmem, stream>>>(A, P);
+    return cudaGetLastError();
+  };
+  if (!A.state_only)
+    return A.reverse ? run(linattn_scan_kernel<TIn, true, true>, P.nseg) : run(linattn_scan_kernel<TIn, false, true>, P.nseg);
+  return A.reverse ? run(linattn_scan_kernel<TIn, true, false>, P.nseg - 1)
+                   : run(linattn_scan_kernel<TIn, false, false>, P.nseg - 1);
+}
+
+template <typename TIn>
+cudaError_t launch_linattn_join(const lin::Pass<TIn> &A, const lin::Shape &P, int B, cudaStream_t stream) {
+  lin::linattn_join_kernel<TIn><<<dim3(P.H, B, 4), 256, 0, stream>>>(A, P);
+  return cudaGetLastError();
+}
+
+template cudaError_t launch_linattn_scan<float>(const lin::Pass<float> &, const lin::Shape &, int, cudaStream_t);
+template cudaError_t launch_linattn_scan<uint16_t>(const lin::Pass<uint16_t> &, const lin::Shape &, int, cudaStream_t);
+template cudaError_t launch_linattn_join<float>(const lin::Pass<float> &, const lin::Shape &, int, cudaStream_t);
+template cudaError_t launch_linattn_join<uint16_t>(const lin::Pass<uint16_t> &, const lin::Shape &, int, cudaStream_t);
+
+}  // namespace rwkv7

@@ -16,7 +16,7 @@ __device__ int g_error_word = 0;
 
 namespace {
 
-constexpr int kVersion = 200;  // 0.2.0: adds the host-buffer prefill
+constexpr int kVersion = 300;  // 0.3.0: adds the head-decay linear attention and the layer norm
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
