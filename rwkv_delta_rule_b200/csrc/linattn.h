@@ -77,6 +77,9 @@ cudaError_t launch_linattn_scan(const lin::Pass<TIn> &pass, const lin::Shape &sh
 // only those, so s_in may be s_out.
 template <typename TIn>
 cudaError_t launch_linattn_join(const lin::Pass<TIn> &pass, const lin::Shape &shape, int B, cudaStream_t stream);
+// The same pass on the tensor cores (linattn_chunk.cu); total_T > 0.  err_word: where its bounded waits report.
+cudaError_t launch_linattn_chunk(const lin::Pass<uint16_t> &pass, const lin::Shape &shape, int B, int *err_word,
+                                 cudaStream_t stream);
 template <typename TIn>
 cudaError_t launch_linattn_decode(const TIn *r, const TIn *k, const TIn *v, const float *w, float *s, TIn *y, int B,
                                   int H, cudaStream_t stream);

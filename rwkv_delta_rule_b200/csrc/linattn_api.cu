@@ -2,6 +2,7 @@
 // norm (include/rwkv7.h): host-side checks, the split of a sequence into segments, launches.
 #include "../../include/rwkv7.h"
 #include "common.cuh"
+#include "launch.h"
 #include "layer_norm.h"
 #include "linattn.h"
 
@@ -15,10 +16,14 @@ rwkv7_status from_cuda(cudaError_t e) { return e == cudaSuccess ? RWKV7_OK : RWK
 
 constexpr long long kStateBytes = kN * kN * sizeof(float);
 
+// bf16 passes run on the tensor cores from this length on.
+constexpr long long kChunkMinT = 32;
+template <typename TIn> bool use_chunk(long long max_T) { return sizeof(TIn) == 2 && max_T >= kChunkMinT; }
+
 // Segments a sequence of at most T tokens is split into, for `pairs` chains: as many as fill the CTAs
-// that the device runs at once (4 per SM).
-int segments(long long pairs, long long T) {
-  const long long want = 592 / pairs, most = T / 128;
+// that the device runs at once (2 per SM on the tensor cores, 4 of the token-by-token kernel).
+int segments(long long pairs, long long T, bool chunk) {
+  const long long want = (chunk ? 296 : 592) / pairs, most = T / 128;
   const long long n = want < most ? want : most;
   return n < 1 ? 1 : static_cast<int>(n);
 }
@@ -27,9 +32,9 @@ long long pass_bytes(long long pairs, int nseg) { return nseg > 1 ? pairs * nseg
 
 // Splits for the workspace given: fewer segments where it holds no more.
 lin::Shape shape(const float *w, const int32_t *cu, int B, int T, long long total_T, long long max_T, int H,
-                 long long bytes, int passes) {
+                 long long bytes, int passes, bool chunk) {
   const long long pairs = static_cast<long long>(B) * H;
-  int n = segments(pairs, max_T);
+  int n = segments(pairs, max_T, chunk);
   const long long room = bytes / (passes * pairs * kStateBytes);
   if (n > room) n = room < 2 ? 1 : static_cast<int>(room);
   const long long len = (((max_T + n - 1) / n) + 127) / 128 * 128;
@@ -37,15 +42,24 @@ lin::Shape shape(const float *w, const int32_t *cu, int B, int T, long long tota
   return lin::Shape{w, cu, T, total_T, H, n, n > 1 ? static_cast<int>(len) : 0x7fffff80};
 }
 
-template <typename TIn> cudaError_t run_pass(lin::Pass<TIn> p, const lin::Shape &s, int B, cudaStream_t stream) {
+template <typename TIn> cudaError_t one_pass(const lin::Pass<TIn> &p, const lin::Shape &s, int B, bool chunk,
+                                             cudaStream_t stream) {
+  if constexpr (sizeof(TIn) == 2) {
+    if (chunk) return launch_linattn_chunk(p, s, B, device_error_word(), stream);
+  }
+  return launch_linattn_scan(p, s, B, stream);
+}
+
+template <typename TIn> cudaError_t run_pass(lin::Pass<TIn> p, const lin::Shape &s, int B, bool chunk,
+                                             cudaStream_t stream) {
   if (s.nseg > 1) {
     lin::Pass<TIn> own = p;
     own.state_only = 1;
-    cudaError_t e = launch_linattn_scan(own, s, B, stream);
+    cudaError_t e = one_pass(own, s, B, chunk, stream);
     if (e == cudaSuccess) e = launch_linattn_join(own, s, B, stream);
     if (e != cudaSuccess) return e;
   }
-  return launch_linattn_scan(p, s, B, stream);
+  return one_pass(p, s, B, chunk, stream);
 }
 
 template <typename TIn>
@@ -66,9 +80,10 @@ rwkv7_status prefill(int B, int T, long long total_T, long long max_T, int H, in
                      long long ws_bytes, rwkv7_stream_t stream) {
   const rwkv7_status st = check(B, total_T, H, N, r, k, v, w, s_in, y, s_out, ws, ws_bytes);
   if (st != RWKV7_OK) return st;
-  const lin::Shape s = shape(w, cu, B, T, total_T, max_T, H, ws_bytes, 1);
+  const bool chunk = use_chunk<TIn>(max_T) && total_T > 0;
+  const lin::Shape s = shape(w, cu, B, T, total_T, max_T, H, ws_bytes, 1, chunk);
   const lin::Pass<TIn> p{r, k, v, y, s_in, s_out, 0, 0, static_cast<float *>(ws), 0, 0};
-  return from_cuda(run_pass(p, s, B, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(run_pass(p, s, B, chunk, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 template <typename TIn>
@@ -118,7 +133,8 @@ extern "C" {
 long long rwkv7_linattn_workspace(int B, int max_T, int H) {
   if (B <= 0 || H <= 0 || max_T <= 0) return 0;
   const long long pairs = static_cast<long long>(B) * H;
-  return pass_bytes(pairs, segments(pairs, max_T));
+  const int a = segments(pairs, max_T, false), b = segments(pairs, max_T, true);
+  return pass_bytes(pairs, a > b ? a : b);
 }
 
 long long rwkv7_linattn_backward_workspace(int B, int T, int H) { return 3 * rwkv7_linattn_workspace(B, T, H); }
@@ -179,7 +195,8 @@ rwkv7_status rwkv7_linattn_backward_bf16(int B, int T, int H, int N, const uint1
     return from_cuda(ds_out ? cudaMemcpyAsync(ds_in, ds_out, bytes, cudaMemcpyDeviceToDevice, cs)
                             : cudaMemsetAsync(ds_in, 0, bytes, cs));
   }
-  const lin::Shape s = shape(w, nullptr, B, T, tokens, T, H, workspace_bytes, 3);
+  const bool chunk = use_chunk<uint16_t>(T);
+  const lin::Shape s = shape(w, nullptr, B, T, tokens, T, H, workspace_bytes, 3, chunk);
   float *ws = static_cast<float *>(workspace);
   const long long part = s.nseg > 1 ? static_cast<long long>(B) * H * s.nseg * kN * kN : 0;
   const lin::Pass<uint16_t> passes[3] = {
@@ -188,7 +205,7 @@ rwkv7_status rwkv7_linattn_backward_bf16(int B, int T, int H, int N, const uint1
       {k, r, dy, dv, ds_out, ds_in, 0, 0, ws + 2 * part, 1, 0},
   };
   for (const lin::Pass<uint16_t> &p : passes) {
-    const cudaError_t e = run_pass(p, s, B, cs);
+    const cudaError_t e = run_pass(p, s, B, chunk, cs);
     if (e != cudaSuccess) return RWKV7_ERR_CUDA;
   }
   return RWKV7_OK;
