@@ -11,18 +11,18 @@
 //     S_0   = w^L S0 + sum_s (w^(s+1) v_s) k_s^T.
 // Only powers w^0 .. w^128 of the head's decay appear, all <= 1, so every w in [0, 1] is exact.
 //
-// One CTA of 128 threads walks the chunks of one (b, h) (or of one segment of it); thread t owns token
-// row t and TMEM lane t.  Per chunk, on the tensor cores with float32 accumulation:
-//     MMA1  [128 x 128] = Q K^T                      Q, K as TMA left them (K-major)
-//     MMA2  [128 x 64]  = Q S0^T                     S0 in two bf16 terms
-//     MMA3  [128 x 64]  = P V                        P from TMEM in bf16, V as TMA left it (MN-major)
-//     MMA4  [128 x 64]  = [V'; V''] K (+ V''' twice)   V' = w^(L-1-s) v_s, see below
-// The state stays in float32 registers across chunks (32 elements per thread).  Roundings to bf16:
+// One CTA of eight warps walks the chunks of one (b, h) (or of one segment of it), two CTAs per SM (so
+// 128 registers a thread, which the kernel needs without spilling).  Warp w has token rows (TMEM lanes)
+// 32 (w % 4) .. + 31 and half w / 4 of their columns; the warp with the least to do in P also issues the
+// TMA loads and the MMAs.  Per chunk, float32 accumulation:
+//     MMA1  [128 x 256] = Q [K; S0 hi; S0 lo]^T      K-major tiles, as TMA and the compute warps left them
+//     MMA2  [128 x 64] += P V                        P from TMEM in bf16, V as TMA left it (MN-major)
+//     MMA3  [128 x 64]  = [V1; V2] K, then + V3 K on both halves      (V1 + V2 + 2 V3 = w^(L-1-s) v_s)
+// The state stays in float32 registers across chunks (16 elements per thread).  Roundings to bf16:
 //   P: one per product, as large as the rounding of out itself, and averaged over the tokens;
-//   S0 in MMA2: hi + lo, 2^-17 of each element; it reaches out only;
-//   w^(L-1-s) v_s in MMA4: hi + mid + lo (2^-25), because these sums are the state: two terms were
-//   2.7e-6 off on average, three are within float32's own rounding.  hi and mid are the two halves of
-//   MMA4's 128 rows; half of lo is added to both by a second pass, and the halves are added in float32.
+//   S0 in MMA1: hi + lo, 2^-16 of each element at most; it reaches out only;
+//   w^(L-1-s) v_s in MMA3: three terms, 2^-24 at most, because these sums are the state: with two terms
+//   they would be 2.7e-6 off on average, the three leave 4e-7 (float32 sums of products alone: 2e-7).
 // k, q and v enter their products as they are, exactly.
 #include <cuda.h>
 
@@ -33,40 +33,93 @@ namespace rwkv7 {
 namespace lin {
 
 constexpr int kChunk = 128;
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr uint32_t kMaxPolls = 1u << 22;
 constexpr uint32_t kTile = kChunk * kN * 2;  // one bf16 128 x 64 tile, 128-byte swizzled rows
 
-// TMEM columns: MMA1's result; P (bf16 pairs) replaces its first half as it is read, MMA3's result its second
-constexpr uint32_t TM_P = 0, TM_Y1 = 64, TM_Y2 = 128, TM_X = 192, kTmemCols = 256;
+// TMEM columns.  MMA1 fills 0 .. 255 (q k, then q S0 hi, q S0 lo); P (bf16 pairs) replaces the first 64 of
+// the products, the state's part of out, on which MMA2 accumulates, the second 64, MMA3's result the
+// S0 lo part: each has been read by then.
+constexpr uint32_t TM_P = 0, TM_Y1 = 64, TM_HI = 128, TM_LO = 192, TM_X = 192, kTmemCols = 256;
 
-// shared memory, from a 1024-aligned base.  Q's tile takes V''' once MMA1 and MMA2 are through with it;
-// V' is where the threads swap halves of MMA4's result afterwards, V'' where out waits for its TMA store.
-constexpr uint32_t OFF_Q = 0, OFF_K = kTile, OFF_V = 2 * kTile, OFF_V1 = 3 * kTile, OFF_V2 = 4 * kTile;
-constexpr uint32_t OFF_S = 5 * kTile;                // hi, then lo: [64 value channels][64 key channels]
+// shared memory, from a 1024-aligned base.  Q's tile takes V3 once MMA1 is through with it; V1's is where
+// the threads swap halves of MMA3's result afterwards, V2's where they put the rows of out together.
+constexpr uint32_t OFF_Q = 0, OFF_K = kTile;
+constexpr uint32_t OFF_S = 2 * kTile;  // hi, then lo: [64 value channels][64 key channels]; MMA1's rows behind K
 constexpr uint32_t kStateTile = kN * kN * 2;
-constexpr uint32_t OFF_PW = OFF_S + 2 * kStateTile;  // float2 [129]: w^n as a float32 and what that leaves
-constexpr uint32_t OFF_BAR = OFF_PW + 1040;          // three mbarriers, TMEM address, abort flag
+constexpr uint32_t OFF_V = OFF_S + 2 * kStateTile, OFF_V1 = OFF_V + kTile, OFF_V2 = OFF_V1 + kTile;
+constexpr uint32_t OFF_CF = OFF_V2 + kTile;  // float [32]: w^(31-x), reversed w^x
+constexpr uint32_t OFF_ZERO = OFF_CF + 128;  // float [32]: zeros, the powers with negative exponents
+constexpr uint32_t OFF_PW = OFF_ZERO + 128;  // float [132]: w^n for n <= 128
+constexpr uint32_t OFF_PL = OFF_PW + 528;    // float [132]: what the rounding of w^n to float32 leaves
+constexpr uint32_t OFF_BAR = OFF_PL + 528;   // mbarriers, TMEM address, flags
 constexpr uint32_t kSmemBytes = OFF_BAR + 64 + 1024;
+// tiles landed; all warps ready for MMA1; MMA1 done; all warps ready for MMA2 and 3; those done
+enum { B_FULL = 0, B_READY = 1, B_M1 = 2, B_P = 3, B_M2 = 4, kBars = 5 };
 
 struct Maps {
-  CUtensorMap q, k, v, out;  // [tokens, H, 64] bf16, box {64, 1, 128}
+  CUtensorMap q, k, v;  // [tokens, H, 64] bf16, box {64, 1, 128}
 };
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+// two float32 values in a register pair, and the packed operations on them (one instruction each)
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 make2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ float lo_of(uint32_t p) { return __uint_as_float(p << 16); }
-__device__ __forceinline__ float hi_of(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
-
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *smem_src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(smem_src)), "r"(c0), "r"(c1), "r"(c2)
+__device__ __forceinline__ void split2(f32x2 x, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) { return fma2(b, make2(-1.f, -1.f), a); }
+// the values cut to their upper 16 bits, which are bf16: what is cut off is left exactly by sub2
+__device__ __forceinline__ f32x2 cut2(f32x2 x) { return x & 0xffff0000ffff0000ull; }
+__device__ __forceinline__ uint32_t high_halves(f32x2 x) {
+  return __byte_perm(static_cast<uint32_t>(x), static_cast<uint32_t>(x >> 32), 0x7632);
+}
+// rounded to nearest-even bf16, the first value in the low half
+__device__ __forceinline__ uint32_t pack2(f32x2 x) {
+  float a, b;
+  split2(x, a, b);
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+// shared memory by 32-bit address
+__device__ __forceinline__ void sts128(uint32_t p, const uint32_t (&u)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
                : "memory");
+}
+__device__ __forceinline__ void sts128f(uint32_t p, const float *u) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(p), "f"(u[0]), "f"(u[1]), "f"(u[2]), "f"(u[3])
+               : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t p, uint32_t (&u)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(p)
+               : "memory");
+}
+__device__ __forceinline__ float lds32(uint32_t p) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
 
 template <bool kRev, bool kOut>
@@ -74,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
                                                                     const Pass<uint16_t> A, const Shape P,
                                                                     int *err_word) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;  // shared-memory addresses from here on
+  uint8_t *smem = smem_raw + (sm - smem_u32(smem_raw));
   const int h = blockIdx.x, b = blockIdx.y, z = blockIdx.z + (!kOut && kRev ? 1 : 0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
@@ -83,282 +137,343 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
   if (!kOut && (kRev ? sg.first : sg.last)) return;
   const long long pair = static_cast<long long>(b) * P.H + h;
 
-  float2 *pw = reinterpret_cast<float2 *>(smem + OFF_PW);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + OFF_BAR);  // tiles landed, MMA1 + MMA2 done, MMA3 + MMA4 done
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_BAR + 32);
-  volatile int *bad = reinterpret_cast<volatile int *>(smem + OFF_BAR + 40);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_BAR + 8 * kBars);
+  volatile int *bad = reinterpret_cast<volatile int *>(smem + OFF_BAR + 8 * kBars + 4);  // a wait ran out
+  volatile int *stop = bad + 1;  // tid 0's copy of it, which all warps act on together
 
   const int nchunks = (sg.len + kChunk - 1) / kChunk;
   auto chunk_at = [&](int i) { return kRev ? nchunks - 1 - i : i; };
-  auto load_tiles = [&](int c) {
-    const int tok = static_cast<int>(sg.lo) + c * kChunk;
-    tc::mbar_arrive_expect_tx(bars, (kOut ? 3 : 2) * kTile);
-    tc::tma_load_3d(smem + OFF_K, &maps.k, bars, 0, h, tok);
-    if (kOut) tc::tma_load_3d(smem + OFF_Q, &maps.q, bars, 0, h, tok);
-    tc::tma_load_3d(smem + OFF_V, &maps.v, bars, 0, h, tok);
+  auto load_tiles = [&](int it) {
+    int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk;
+    tc::mbar_arrive_expect_tx(bars + B_FULL, (kOut ? 3 : 2) * kTile);
+    tc::tma_load_3d(smem + OFF_V, &maps.v, bars + B_FULL, 0, h, tok);
+    tc::tma_load_3d(smem + OFF_K, &maps.k, bars + B_FULL, 0, h, tok);
+    if (kOut) tc::tma_load_3d(smem + OFF_Q, &maps.q, bars + B_FULL, 0, h, tok);
+    if (it + 1 < nchunks) {  // the next ones on their way to L2
+      tok += kRev ? -kChunk : kChunk;
+      tc::tma_prefetch_l2_3d(&maps.v, 0, h, tok);
+      tc::tma_prefetch_l2_3d(&maps.k, 0, h, tok);
+      if (kOut) tc::tma_prefetch_l2_3d(&maps.q, 0, h, tok);
+    }
   };
-  if (tid == 0) {
-    for (int i = 0; i < 3; ++i) tc::mbar_init(bars + i, 1);
-    tc::fence_mbar_init();
-    *bad = 0;
-    if (nchunks > 0) load_tiles(chunk_at(0));
-  }
-  if (warp == 0) {
+  constexpr int kLead = kRev ? 3 : 4;  // its rows have no products, or one group of them
+  if (warp == kLead) {
+    if (lane == 0) {
+      for (int i = 0; i < kBars; ++i) tc::mbar_init(bars + i, i == B_READY || i == B_P ? 8 : 1);
+      tc::fence_mbar_init();
+      *bad = 0;
+      *stop = 0;
+      if (nchunks > 0) load_tiles(0);
+    }
+    __syncwarp();
     tc::tmem_alloc(tmem_slot, kTmemCols);
     tc::tmem_relinquish();
   }
-  for (int n = tid; n <= kChunk; n += kThreads) {
-    const double p = powi(static_cast<double>(P.w[h]), n);
-    const float f = static_cast<float>(p);
-    pw[n] = make_float2(f, static_cast<float>(p - static_cast<double>(f)));
+  {
+    float *cf = reinterpret_cast<float *>(smem + OFF_CF), *pw = reinterpret_cast<float *>(smem + OFF_PW);
+    float *pl = reinterpret_cast<float *>(smem + OFF_PL);
+    if (tid < 32) reinterpret_cast<float *>(smem + OFF_ZERO)[tid] = 0.f;
+    for (int n = tid; n <= kChunk; n += kThreads) {
+      const double p = powi(static_cast<double>(P.w[h]), n);
+      const float f = static_cast<float>(p);
+      pw[n] = f;
+      pl[n] = static_cast<float>(p - static_cast<double>(f));
+      if (n < 32) cf[kRev ? n : 31 - n] = f;
+    }
   }
 
-  // this thread's part of the state: row i (value channel), columns 32 half .. + 31
-  const int i = tid & 63, half = tid >> 6;
-  float S[32];
+  const int rb = warp & 3, half = warp >> 2;  // row block and column half of this warp
+  const int row = 32 * rb + lane;
+  // chunk x of this thread's half row of a swizzled tile is at tile + (at ^ 16 x)
+  const uint32_t at = sm + row * 128u + (((4 * half) ^ (row & 7)) << 4);
+  // this thread's part of the state: row i (value channel), columns j0 .. j0 + 15.  Rows 0 .. 63 of MMA3's
+  // result are V1 K, rows 64 .. 127 V2 K: thread (row, half) sees columns 32 half .. + 31 of one of them,
+  // keeps 16 of those and swaps the others with thread (row ^ 64, half).
+  const bool upper = rb >= 2;
+  const int i = row & 63, j0 = 32 * half + (upper ? 16 : 0);
+  const uint32_t at_s = sm + OFF_S + i * 128u + (((j0 >> 3) ^ (i & 7)) << 4);
+  f32x2 S[8];
+  auto put_state = [&]() {  // S as two bf16 terms, rows of MMA1's B operand
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f32x2 s = S[4 * c + e];
+        hi[e] = high_halves(s);
+        lo[e] = pack2(sub2(s, cut2(s)));
+      }
+      sts128(at_s ^ (16 * c), hi);
+      sts128((at_s ^ (16 * c)) + kStateTile, lo);
+    }
+  };
   {
     const float *from = !kOut ? nullptr : P.nseg > 1 ? A.ws + (pair * P.nseg + z) * (kN * kN) : A.s_in;
     if (kOut && P.nseg == 1 && from != nullptr) from += pair * (kN * kN);
     const int t = P.nseg == 1 && A.s_in_t;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) S[e] = from == nullptr ? 0.f : from[state_at(t, i, 32 * half + e)];
+    for (int e = 0; e < 8; ++e)
+      S[e] = from == nullptr ? make2(0.f, 0.f)
+                             : make2(from[state_at(t, i, j0 + 2 * e)], from[state_at(t, i, j0 + 2 * e + 1)]);
+    if (kOut) put_state();
   }
-  auto put_state = [&]() {  // S as two bf16 terms, the B operand of MMA2
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = S[8 * c + 2 * e], y = S[8 * c + 2 * e + 1];
-        hi[e] = pack2(x, y);
-        lo[e] = pack2(x - lo_of(hi[e]), y - hi_of(hi[e]));
-      }
-      uint8_t *p = smem + OFF_S + tc::sw128(i, 4 * half + c);
-      *reinterpret_cast<uint4 *>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4 *>(p + kStateTile) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-  };
-  if (kOut) put_state();
-  tc::fence_proxy_async_smem();
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tml = tmem + (static_cast<uint32_t>(warp) << 21);  // this warp's lanes
-  const uint32_t sQ = smem_u32(smem + OFF_Q), sK = smem_u32(smem + OFF_K), sV = smem_u32(smem + OFF_V);
-  const uint32_t sV1 = smem_u32(smem + OFF_V1), sS = smem_u32(smem + OFF_S);
-  int waited[3] = {0, 0, 0}, begun[3] = {nchunks > 0 ? 1 : 0, 0, 0};  // phases of the barriers (begun: thread 0's view)
-  auto wait = [&](int k) {
-    if (!tc::mbar_wait_bounded(bars + k, waited[k] & 1, kMaxPolls)) {
-      *bad = 1;
-      return;
+
+  // Bounded wait for phase n of a barrier.  After a wait has run out anywhere in the CTA, all others
+  // return at once: the warps finish their chunk (on whatever is there, within bounds), so that every
+  // named barrier is reached by all, and stop together at its end.
+  auto wait = [&](int k, int n) -> bool {
+    for (uint32_t p = 0; p < kMaxPolls; ++p) {
+      if (tc::mbar_try_wait(bars + k, n & 1)) return true;
+      if ((p & 63u) == 63u && *bad) return false;
     }
-    ++waited[k];
+    *bad = 1;
+    return false;
   };
 
+  int m1 = 0, m2 = 0, full = nchunks > 0 ? 1 : 0;  // phases under way (the leading lane's view)
+  const uint32_t tml = tmem + (static_cast<uint32_t>(rb) << 21);  // this warp's lanes
   for (int it = 0; it < nchunks; ++it) {
     const int c = chunk_at(it), L = min(kChunk, sg.len - c * kChunk);
-    wait(0);
+    wait(B_FULL, it);
     if (L < kChunk) {
       // rows past the end hold other sequences' tokens: K and V count as zero there (Q's rows give
       // outputs that are not stored)
-      if (tid >= L) {
+      if (row >= L) {
+        const uint32_t zero[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          *reinterpret_cast<uint4 *>(smem + OFF_K + tid * 128 + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4 *>(smem + OFF_V + tid * 128 + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
+        for (int x = 0; x < 4; ++x) {
+          sts128((at ^ (16 * x)) + OFF_K, zero);
+          sts128((at ^ (16 * x)) + OFF_V, zero);
         }
       }
-      tc::fence_proxy_async_smem();
-      __syncthreads();
     }
     if (kOut) {
-      if (tid == 0 && !*bad) {
-        tc::tc_fence_after();
-        constexpr uint32_t d1 = tc::instr_desc(tc::kFmtBF16, 128, 128, false, false);
-        constexpr uint32_t d2 = tc::instr_desc(tc::kFmtBF16, 128, 64, false, false);
+      tc::fence_proxy_async_smem();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bars + B_READY);
+      if (warp == kLead) {
+        if (lane == 0 && wait(B_READY, it)) {
+          tc::tc_fence_after();
+          constexpr uint32_t d1 = tc::instr_desc(tc::kFmtBF16, 128, 256, false, false);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc::mma_ss(0, tmem + TM_P, tc::smem_desc(sQ + ks * 32, 16, 1024), tc::smem_desc(sK + ks * 32, 16, 1024), d1,
-                     ks > 0);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc::mma_ss(0, tmem + TM_Y2, tc::smem_desc(sQ + (ks & 3) * 32, 16, 1024),
-                     tc::smem_desc(sS + (ks >> 2) * kStateTile + (ks & 3) * 32, 16, 1024), d2, ks > 0);
-        tc::mma_commit(bars + 1);
-        begun[1]++;
+          for (int ks = 0; ks < 4; ++ks)
+            tc::mma_ss(0, tmem + TM_P, tc::smem_desc(sm + OFF_Q + ks * 32, 16, 1024),
+                       tc::smem_desc(sm + OFF_K + ks * 32, 16, 1024), d1, ks > 0);
+          tc::mma_commit(bars + B_M1);
+          ++m1;
+        }
+        __syncwarp();
       }
-      // the last chunk's outputs have left V''
-      if (tid == 0) bulk_wait_read();
-      __syncthreads();
-      if (*bad) break;
     }
 
-    // V', V'' and V''': token row tid scaled and split
-    uint32_t third[32];
+    // V1, V2 and V3: this thread's half of its token row, scaled and cut into 8-bit pieces
+    uint32_t third[16];
     {
-      const float f = pw[kRev ? min(tid + 1, kChunk) : max(L - 1 - tid, 0)].x;
+      const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? row + 1 : max(L - 1 - row, 0)));
+      const f32x2 f = make2(f1, f1), half_ = make2(0.5f, 0.5f), mhalf = make2(-0.5f, -0.5f);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const uint32_t at = tc::sw128(tid, x);
-        const uint4 u = *reinterpret_cast<const uint4 *>(smem + OFF_V + at);
-        const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-        uint32_t p1[4], p2[4];
+      for (int x = 0; x < 4; ++x) {
+        uint32_t in[4], p1[4], p2[4];
+        lds128((at ^ (16 * x)) + OFF_V, in);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float a = lo_of(in[e]) * f, bb = hi_of(in[e]) * f;
-          p1[e] = pack2(a, bb);
-          a -= lo_of(p1[e]);
-          bb -= hi_of(p1[e]);
-          p2[e] = pack2(a, bb);
-          third[4 * x + e] = pack2(0.5f * (a - lo_of(p2[e])), 0.5f * (bb - hi_of(p2[e])));
+          const f32x2 v = mul2(make2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), f);
+          p1[e] = high_halves(v);
+          const f32x2 r = sub2(v, cut2(v));
+          p2[e] = high_halves(r);
+          third[4 * x + e] = high_halves(fma2(cut2(r), mhalf, mul2(r, half_)));
         }
-        *reinterpret_cast<uint4 *>(smem + OFF_V1 + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-        *reinterpret_cast<uint4 *>(smem + OFF_V2 + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+        sts128((at ^ (16 * x)) + OFF_V1, p1);
+        sts128((at ^ (16 * x)) + OFF_V2, p2);
       }
     }
     if (kOut) {
-      wait(1);
+      wait(B_M1, it);
       tc::tc_fence_after();
     }
 #pragma unroll
-    for (int x = 0; x < 8; ++x)
-      *reinterpret_cast<uint4 *>(smem + OFF_Q + tc::sw128(tid, x)) =
-          make_uint4(third[4 * x], third[4 * x + 1], third[4 * x + 2], third[4 * x + 3]);
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t p3[4] = {third[4 * x], third[4 * x + 1], third[4 * x + 2], third[4 * x + 3]};
+      sts128((at ^ (16 * x)) + OFF_Q, p3);
+    }
     if (kOut) {
-      // P, 32 columns at a time: P's columns are behind those still to be read
+      // P: column groups half and half + 2, 32 columns each.  Both halves' warps have read their
+      // products before either overwrites columns.
+      float pk[2][16];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float pk[16];
-        if (g == warp || (kRev ? g > warp : g < warp)) {
+      for (int n = 0; n < 2; ++n) {
+        const int g = half + 2 * n;
+        if (g == rb) {
+          // w^(t-s), or zero past the diagonal: powers with 32 zeros in front
           float v[32];
           tc::tmem_ld32(tml + TM_P + 32 * g, v);
-          if (g == warp) {
+          const uint32_t d = sm + OFF_PW + (kRev ? -4 * lane : 4 * lane);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const int d = kRev ? x - lane : lane - x;
-              v[x] = d >= 0 ? v[x] * pw[d].x : 0.f;
-            }
-          } else {
-            // w^(t-s) = w^(t - 32 g - 31) w^(31 - x), reversed w^(s-t) = w^(32 g - t) w^x
-            const float a = pw[kRev ? 32 * g - tid : tid - 32 * g - 31].x;
+          for (int x = 0; x < 16; ++x)
+            pk[n][x] = __uint_as_float(pack2(mul2(make2(v[2 * x], v[2 * x + 1]),
+                                                  make2(lds32(d + (kRev ? 8 * x : -8 * x)),
+                                                        lds32(d + (kRev ? 8 * x + 4 : -8 * x - 4))))));
+        } else if (kRev ? g > rb : g < rb) {
+          // w^(t-s) = w^(t - 32 g - 31) w^(31 - x), reversed w^(s-t) = w^(32 g - t) w^x
+          float v[32];
+          tc::tmem_ld32(tml + TM_P + 32 * g, v);
+          const float a1 = lds32(sm + OFF_PW + 4 * (kRev ? 32 * g - row : row - 32 * g - 31));
+          const f32x2 a = make2(a1, a1);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = v[x] * a * pw[kRev ? x : 31 - x].x;
+          for (int x = 0; x < 8; ++x) {
+            uint32_t f[4];
+            lds128(sm + OFF_CF + 16 * x, f);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              pk[n][2 * x + e] = __uint_as_float(
+                  pack2(mul2(make2(v[4 * x + 2 * e], v[4 * x + 2 * e + 1]),
+                             mul2(make2(__uint_as_float(f[2 * e]), __uint_as_float(f[2 * e + 1])), a))));
           }
-#pragma unroll
-          for (int x = 0; x < 16; ++x) pk[x] = __uint_as_float(pack2(v[2 * x], v[2 * x + 1]));
         } else {
 #pragma unroll
-          for (int x = 0; x < 16; ++x) pk[x] = 0.f;
+          for (int x = 0; x < 16; ++x) pk[n][x] = 0.f;
         }
-        tc::tmem_st16(tml + TM_P + 16 * g, pk);
+      }
+      named_sync(1 + rb, 64);
+      tc::tmem_st16(tml + TM_P + 16 * half, pk[0]);
+      tc::tmem_st16(tml + TM_P + 16 * (half + 2), pk[1]);
+      // the state's part of the outputs, which MMA2 adds to
+      const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? max(L - 1 - row, 0) : row + 1));
+      const f32x2 f = make2(f1, f1);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        float y[16], v[16];
+        tc::tmem_ld16(tml + TM_HI + 32 * half + 16 * n, y);
+        tc::tmem_ld16(tml + TM_LO + 32 * half + 16 * n, v);
+#pragma unroll
+        for (int x = 0; x < 16; x += 2)
+          split2(mul2(add2(make2(y[x], y[x + 1]), make2(v[x], v[x + 1])), f), y[x], y[x + 1]);
+        tc::tmem_st16(tml + TM_Y1 + 32 * half + 16 * n, y);
       }
       tc::tmem_st_wait();
       tc::tc_fence_before();
     }
     tc::fence_proxy_async_smem();
-    __syncthreads();
-    if (*bad) break;
-    if (tid == 0) {
-      tc::tc_fence_after();
-      constexpr uint32_t d3 = tc::instr_desc(tc::kFmtBF16, 128, 64, false, true);
-      constexpr uint32_t d4 = tc::instr_desc(tc::kFmtBF16, 128, 64, true, true);
-      if (kOut) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bars + B_P);
+    if (warp == kLead) {
+      if (lane == 0 && wait(B_P, it)) {
+        tc::tc_fence_after();
+        constexpr uint32_t d2 = tc::instr_desc(tc::kFmtBF16, 128, 64, false, true);
+        constexpr uint32_t d3 = tc::instr_desc(tc::kFmtBF16, 128, 64, true, true);
+        if (kOut) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc::mma_ts_bf16(tmem + TM_Y1, tmem + TM_P + 8 * ks, tc::smem_desc(sV + ks * 2048, kTile, 1024), d3, ks > 0);
+          for (int ks = 0; ks < 8; ++ks)
+            tc::mma_ts_bf16(tmem + TM_Y1, tmem + TM_P + 8 * ks, tc::smem_desc(sm + OFF_V + ks * 2048, kTile, 1024), d2,
+                            1);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks)  // V1 over V2; then V3 over itself (block stride 0)
+          tc::mma_ss(0, tmem + TM_X,
+                     tc::smem_desc(sm + (ks < 8 ? OFF_V1 : OFF_Q) + (ks & 7) * 2048, ks < 8 ? kTile : 0, 1024),
+                     tc::smem_desc(sm + OFF_K + (ks & 7) * 2048, kTile, 1024), d3, ks > 0);
+        tc::mma_commit(bars + B_M2);
+        ++m2;
       }
-#pragma unroll
-      for (int ks = 0; ks < 16; ++ks)  // V' over V''; then V''' over itself (block stride 0)
-        tc::mma_ss(0, tmem + TM_X, tc::smem_desc((ks < 8 ? sV1 : sQ) + (ks & 7) * 2048, ks < 8 ? kTile : 0, 1024),
-                   tc::smem_desc(sK + (ks & 7) * 2048, kTile, 1024), d4, ks > 0);
-      tc::mma_commit(bars + 2);
-      begun[2]++;
+      __syncwarp();
     }
-    float y[64];
-    if (kOut) {
-      // meanwhile the state's part of the outputs
-      const float f = pw[kRev ? max(L - 1 - tid, 0) : tid + 1].x;
-      float v[32];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        tc::tmem_ld32(tml + TM_Y2 + 32 * g, v);
-#pragma unroll
-        for (int x = 0; x < 32; ++x) y[32 * g + x] = v[x] * f;
-      }
-    }
-    wait(2);
+
+    wait(B_M2, it);
     tc::tc_fence_after();
-    if (tid == 0 && it + 1 < nchunks && !*bad) {
-      load_tiles(chunk_at(it + 1));
-      begun[0]++;
+    if (warp == kLead && lane == 0 && it + 1 < nchunks && !*bad) {
+      load_tiles(it + 1);
+      ++full;
     }
     {
-      // the two halves of MMA4: this thread keeps its 32 columns and swaps the others with tid ^ 64
-      float mine[32], other[32];
-      tc::tmem_ld32(tml + TM_X + 32 * half, mine);
-      tc::tmem_ld32(tml + TM_X + 32 * (half ^ 1), other);
+      float x32[32];
+      tc::tmem_ld32(tml + TM_X + 32 * half, x32);
+      f32x2 mine[8];
+      // (the same for a whole warp)
+      if (upper) {
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        *reinterpret_cast<float4 *>(smem + OFF_V1 + tc::sw128(tid, x)) =
-            make_float4(other[4 * x], other[4 * x + 1], other[4 * x + 2], other[4 * x + 3]);
-      if (kOut) {
+        for (int x = 0; x < 4; ++x) sts128f((at ^ (16 * x)) + OFF_V1, x32 + 4 * x);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float v[32];
-          tc::tmem_ld32(tml + TM_Y1 + 32 * g, v);
+        for (int e = 0; e < 8; ++e) mine[e] = make2(x32[16 + 2 * e], x32[17 + 2 * e]);
+      } else {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) y[32 * g + x] += v[x];
+        for (int x = 0; x < 4; ++x) sts128f((at ^ (16 * x)) + OFF_V1, x32 + 16 + 4 * x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mine[e] = make2(x32[2 * e], x32[1 + 2 * e]);
+      }
+      named_sync(5 + 2 * half + (rb & 1), 64);
+      const float f1 = lds32(sm + OFF_PW + 4 * L), f2 = lds32(sm + OFF_PL + 4 * L);
+      const f32x2 f = make2(f1, f1), fl = make2(f2, f2);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t u[4];
+        lds128((at ^ (16 * x)) + OFF_V1 + (upper ? -64 * 128 : 64 * 128), u);  // row ^ 64
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const f32x2 o = make2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
+          f32x2 &s = S[2 * x + e];
+          s = fma2(s, f, fma2(s, fl, add2(mine[2 * x + e], o)));
         }
-        uint16_t *row = A.out + ((sg.lo + c * kChunk + tid) * P.H + h) * kN;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const uint4 u = make_uint4(pack2(y[8 * x], y[8 * x + 1]), pack2(y[8 * x + 2], y[8 * x + 3]),
-                                     pack2(y[8 * x + 4], y[8 * x + 5]), pack2(y[8 * x + 6], y[8 * x + 7]));
-          if (L == kChunk)
-            *reinterpret_cast<uint4 *>(smem + OFF_V2 + tc::sw128(tid, x)) = u;
-          else if (tid < L)
-            reinterpret_cast<uint4 *>(row)[x] = u;
-        }
       }
-      tc::fence_proxy_async_smem();
-      __syncthreads();
-      if (kOut && tid == 0 && L == kChunk) {
-        tma_store_3d(&maps.out, smem + OFF_V2, 0, h, static_cast<int>(sg.lo) + c * kChunk);
-        tc::bulk_commit_group();
-      }
-      const float2 f = pw[L];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float4 u = *reinterpret_cast<const float4 *>(smem + OFF_V1 + tc::sw128(tid ^ 64, x));
-        const float o[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[4 * x + e] = fmaf(S[4 * x + e], f.x, fmaf(S[4 * x + e], f.y, mine[4 * x + e] + o[e]));
-      }
-      if (kOut) put_state();
-      tc::fence_proxy_async_smem();
-      tc::tc_fence_before();
-      __syncthreads();
-      if (*bad) break;
     }
+    if (kOut) {
+      put_state();
+      float v[32];
+      tc::tmem_ld32(tml + TM_Y1 + 32 * half, v);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = pack2(make2(v[8 * x + 2 * e], v[8 * x + 2 * e + 1]));
+        sts128((at ^ (16 * x)) + OFF_V2, u);
+      }
+      __syncwarp();
+      // the warp's 32 half rows, 4 lanes to each: rows r0, r0 + 8, ..
+      const int r0 = 32 * rb + (lane >> 2), ch = 4 * half + (lane & 3);
+      uint16_t *out = A.out + ((sg.lo + c * kChunk + r0) * P.H + h) * kN + 8 * ch;
+      const uint32_t from = sm + OFF_V2 + r0 * 128 + ((ch ^ (r0 & 7)) << 4);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        uint32_t u[4];
+        lds128(from + 1024 * n, u);
+        if (r0 + 8 * n < L)
+          *reinterpret_cast<uint4 *>(out + static_cast<long long>(8 * n) * P.H * kN) = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+    tc::tc_fence_before();
+    if (tid == 0) *stop = *bad;
+    named_sync(9, kThreads);
+    if (*stop) break;
   }
-
-  if (*bad && tid == 0) {
+  if (warp == kLead && lane == 0 && *bad) {
     // give up: whatever is still in flight lands first
     report_device_error(err_word, kDevErrTimeout);
-    for (int k = 0; k < 3; ++k)
-      while (waited[k] < begun[k] && tc::mbar_wait_bounded(bars + k, waited[k] & 1, kMaxPolls)) ++waited[k];
+    if (full > 0) tc::mbar_wait_bounded(bars + B_FULL, (full - 1) & 1, kMaxPolls);
+    if (m1 > 0) tc::mbar_wait_bounded(bars + B_M1, (m1 - 1) & 1, kMaxPolls);
+    if (m2 > 0) tc::mbar_wait_bounded(bars + B_M2, (m2 - 1) & 1, kMaxPolls);
   }
-  if (tid == 0) tc::bulk_wait_all();
-  __syncthreads();
-  if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
-
   const bool ends = kRev ? sg.first : sg.last;
   float *to = !kOut ? A.ws + (pair * P.nseg + (kRev ? z - 1 : z + 1)) * (kN * kN)
               : ends && A.s_out != nullptr ? A.s_out + pair * (kN * kN) : nullptr;
   if (to != nullptr) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) to[state_at(kOut && A.s_out_t, i, 32 * half + e)] = S[e];
+    for (int e = 0; e < 8; ++e) {
+      float x, y;
+      split2(S[e], x, y);
+      to[state_at(kOut && A.s_out_t, i, j0 + 2 * e)] = x;
+      to[state_at(kOut && A.s_out_t, i, j0 + 2 * e + 1)] = y;
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == kLead) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -399,10 +514,9 @@ cudaError_t launch_linattn_chunk(const lin::Pass<uint16_t> &A, const lin::Shape 
   const int nz = A.state_only ? P.nseg - 1 : P.nseg;
   if (nz <= 0) return cudaSuccess;
   Maps maps;
-  // a call without outputs loads no q and stores nothing: any valid map does
+  // a call for the states alone loads no q: any valid map does
   if (!make_map(&maps.k, A.k, P.total_T, P.H) || !make_map(&maps.v, A.v, P.total_T, P.H) ||
-      !make_map(&maps.q, A.state_only ? A.k : A.q, P.total_T, P.H) ||
-      !make_map(&maps.out, A.state_only ? static_cast<const void *>(A.k) : A.out, P.total_T, P.H))
+      !make_map(&maps.q, A.state_only ? A.k : A.q, P.total_T, P.H))
     return cudaErrorInvalidValue;
   auto run = [&](auto kern) -> cudaError_t {
     const cudaError_t e =
