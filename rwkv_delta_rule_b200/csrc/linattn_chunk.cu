@@ -15,12 +15,14 @@
 // 128 registers a thread, which the kernel needs without spilling).  Warp w has token rows (TMEM lanes)
 // 32 (w % 4) .. + 31 and half w / 4 of their columns; the warp with the least to do in P also issues the
 // TMA loads and the MMAs.  Per chunk, float32 accumulation:
-//     MMA1  [128 x 256] = Q [K; S0 hi; S0 lo]^T      K-major tiles, as TMA and the compute warps left them
+//     MMA1  [128 x 192] = Q [K; S0]^T                K-major tiles, as TMA and the warps left them
 //     MMA2  [128 x 64] += P V                        P from TMEM in bf16, V as TMA left it (MN-major)
 //     MMA3  [128 x 64]  = [V1; V2] K, then + V3 K on both halves      (V1 + V2 + 2 V3 = w^(L-1-s) v_s)
+// MMA3 and the new state run beside P and MMA2, and Q and K of the next chunk arrive meanwhile.
 // The state stays in float32 registers across chunks (16 elements per thread).  Roundings to bf16:
 //   P: one per product, as large as the rounding of out itself, and averaged over the tokens;
-//   S0 in MMA1: hi + lo, 2^-16 of each element at most; it reaches out only;
+//   S0 in MMA1: once, 2^-8 at most like P; it reaches out only.  A second term cost the 8 KB and the 64
+//   TMEM columns that let MMA3 run early (685 us against @@ at B4 T16384 H64);
 //   w^(L-1-s) v_s in MMA3: three terms, 2^-24 at most, because these sums are the state: with two terms
 //   they would be 2.7e-6 off on average, the three leave 4e-7 (float32 sums of products alone: 2e-7).
 // k, q and v enter their products as they are, exactly.
@@ -37,25 +39,23 @@ constexpr int kThreads = 256;
 constexpr uint32_t kMaxPolls = 1u << 22;
 constexpr uint32_t kTile = kChunk * kN * 2;  // one bf16 128 x 64 tile, 128-byte swizzled rows
 
-// TMEM columns.  MMA1 fills 0 .. 255 (q k, then q S0 hi, q S0 lo); P (bf16 pairs) replaces the first 64 of
-// the products, the state's part of out, on which MMA2 accumulates, the second 64, MMA3's result the
-// S0 lo part: each has been read by then.
-constexpr uint32_t TM_P = 0, TM_Y1 = 64, TM_HI = 128, TM_LO = 192, TM_X = 192, kTmemCols = 256;
+// TMEM columns.  MMA1 fills 0 .. 191 (q k, then q S0); P (bf16 pairs) replaces the first 64 of the
+// products once they have been read; the state's part of out is scaled in place, and MMA2 adds to it.
+constexpr uint32_t TM_P = 0, TM_Y = 128, TM_X = 192, kTmemCols = 256;
 
-// shared memory, from a 1024-aligned base.  Q's tile takes V3 once MMA1 is through with it; V1's is where
-// the threads swap halves of MMA3's result afterwards, V2's where they put the rows of out together.
+// shared memory, from a 1024-aligned base.  V1's tile is where the threads swap halves of MMA3's result
+// afterwards, V2's where they put the rows of out together.
 constexpr uint32_t OFF_Q = 0, OFF_K = kTile;
-constexpr uint32_t OFF_S = 2 * kTile;  // hi, then lo: [64 value channels][64 key channels]; MMA1's rows behind K
-constexpr uint32_t kStateTile = kN * kN * 2;
-constexpr uint32_t OFF_V = OFF_S + 2 * kStateTile, OFF_V1 = OFF_V + kTile, OFF_V2 = OFF_V1 + kTile;
-constexpr uint32_t OFF_CF = OFF_V2 + kTile;  // float [32]: w^(31-x), reversed w^x
+constexpr uint32_t OFF_S = 2 * kTile;  // [64 value channels][64 key channels]; MMA1's rows behind K
+constexpr uint32_t OFF_V = OFF_S + kN * kN * 2, OFF_V1 = OFF_V + kTile, OFF_V2 = OFF_V1 + kTile, OFF_V3 = OFF_V2 + kTile;
+constexpr uint32_t OFF_CF = OFF_V3 + kTile;  // float [32]: w^(31-x), reversed w^x
 constexpr uint32_t OFF_ZERO = OFF_CF + 128;  // float [32]: zeros, the powers with negative exponents
 constexpr uint32_t OFF_PW = OFF_ZERO + 128;  // float [132]: w^n for n <= 128
 constexpr uint32_t OFF_PL = OFF_PW + 528;    // float [132]: what the rounding of w^n to float32 leaves
 constexpr uint32_t OFF_BAR = OFF_PL + 528;   // mbarriers, TMEM address, flags
-constexpr uint32_t kSmemBytes = OFF_BAR + 64 + 1024;
-// tiles landed; all warps ready for MMA1; MMA1 done; all warps ready for MMA2 and 3; those done
-enum { B_FULL = 0, B_READY = 1, B_M1 = 2, B_P = 3, B_M2 = 4, kBars = 5 };
+constexpr uint32_t kSmemBytes = OFF_BAR + 128 + 1024;
+// Tiles landed (Q and K; V); all warps ready for MMA1, MMA3, MMA2; each of those done.
+enum { B_QK, B_V, B_READY, B_SPLIT, B_P, B_M1, B_M3, B_M2, kBars };
 
 struct Maps {
   CUtensorMap q, k, v;  // [tokens, H, 64] bf16, box {64, 1, 128}
@@ -144,27 +144,34 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
 
   const int nchunks = (sg.len + kChunk - 1) / kChunk;
   auto chunk_at = [&](int i) { return kRev ? nchunks - 1 - i : i; };
-  auto load_tiles = [&](int it) {
-    int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk;
-    tc::mbar_arrive_expect_tx(bars + B_FULL, (kOut ? 3 : 2) * kTile);
-    tc::tma_load_3d(smem + OFF_V, &maps.v, bars + B_FULL, 0, h, tok);
-    tc::tma_load_3d(smem + OFF_K, &maps.k, bars + B_FULL, 0, h, tok);
-    if (kOut) tc::tma_load_3d(smem + OFF_Q, &maps.q, bars + B_FULL, 0, h, tok);
-    if (it + 1 < nchunks) {  // the next ones on their way to L2
-      tok += kRev ? -kChunk : kChunk;
-      tc::tma_prefetch_l2_3d(&maps.v, 0, h, tok);
-      tc::tma_prefetch_l2_3d(&maps.k, 0, h, tok);
-      if (kOut) tc::tma_prefetch_l2_3d(&maps.q, 0, h, tok);
+  // Loads of chunk `it`, and the chunk after it on its way to L2.
+  auto load_qk = [&](int it) {
+    const int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk, next = tok + (kRev ? -kChunk : kChunk);
+    tc::mbar_arrive_expect_tx(bars + B_QK, (kOut ? 2 : 1) * kTile);
+    tc::tma_load_3d(smem + OFF_K, &maps.k, bars + B_QK, 0, h, tok);
+    if (kOut) tc::tma_load_3d(smem + OFF_Q, &maps.q, bars + B_QK, 0, h, tok);
+    if (it + 1 < nchunks) {
+      tc::tma_prefetch_l2_3d(&maps.k, 0, h, next);
+      if (kOut) tc::tma_prefetch_l2_3d(&maps.q, 0, h, next);
     }
+  };
+  auto load_v = [&](int it) {
+    const int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk, next = tok + (kRev ? -kChunk : kChunk);
+    tc::mbar_arrive_expect_tx(bars + B_V, kTile);
+    tc::tma_load_3d(smem + OFF_V, &maps.v, bars + B_V, 0, h, tok);
+    if (it + 1 < nchunks) tc::tma_prefetch_l2_3d(&maps.v, 0, h, next);
   };
   constexpr int kLead = kRev ? 3 : 4;  // its rows have no products, or one group of them
   if (warp == kLead) {
     if (lane == 0) {
-      for (int i = 0; i < kBars; ++i) tc::mbar_init(bars + i, i == B_READY || i == B_P ? 8 : 1);
+      for (int i = 0; i < kBars; ++i) tc::mbar_init(bars + i, i >= B_READY && i <= B_P ? 8 : 1);
       tc::fence_mbar_init();
       *bad = 0;
       *stop = 0;
-      if (nchunks > 0) load_tiles(0);
+      if (nchunks > 0) {
+        load_v(0);
+        load_qk(0);
+      }
     }
     __syncwarp();
     tc::tmem_alloc(tmem_slot, kTmemCols);
@@ -194,18 +201,13 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
   const int i = row & 63, j0 = 32 * half + (upper ? 16 : 0);
   const uint32_t at_s = sm + OFF_S + i * 128u + (((j0 >> 3) ^ (i & 7)) << 4);
   f32x2 S[8];
-  auto put_state = [&]() {  // S as two bf16 terms, rows of MMA1's B operand
+  auto put_state = [&]() {  // S in bf16, rows of MMA1's B operand
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      uint32_t hi[4], lo[4];
+      uint32_t u[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const f32x2 s = S[4 * c + e];
-        hi[e] = high_halves(s);
-        lo[e] = pack2(sub2(s, cut2(s)));
-      }
-      sts128(at_s ^ (16 * c), hi);
-      sts128((at_s ^ (16 * c)) + kStateTile, lo);
+      for (int e = 0; e < 4; ++e) u[e] = pack2(S[4 * c + e]);
+      sts128(at_s ^ (16 * c), u);
     }
   };
   {
@@ -235,22 +237,19 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
     return false;
   };
 
-  int m1 = 0, m2 = 0, full = nchunks > 0 ? 1 : 0;  // phases under way (the leading lane's view)
+  // phases under way, for the leading lane to wait out if it has to give up
+  int begun[kBars] = {};
+  if (nchunks > 0) begun[B_QK] = begun[B_V] = 1;
   const uint32_t tml = tmem + (static_cast<uint32_t>(rb) << 21);  // this warp's lanes
   for (int it = 0; it < nchunks; ++it) {
     const int c = chunk_at(it), L = min(kChunk, sg.len - c * kChunk);
-    wait(B_FULL, it);
-    if (L < kChunk) {
-      // rows past the end hold other sequences' tokens: K and V count as zero there (Q's rows give
-      // outputs that are not stored)
-      if (row >= L) {
-        const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+    // rows past the end hold other sequences' tokens: K and V count as zero there (Q's rows give
+    // outputs that are not stored)
+    const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+    wait(B_QK, it);
+    if (row >= L) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          sts128((at ^ (16 * x)) + OFF_K, zero);
-          sts128((at ^ (16 * x)) + OFF_V, zero);
-        }
-      }
+      for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + OFF_K, zero);
     }
     if (kOut) {
       tc::fence_proxy_async_smem();
@@ -260,26 +259,30 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
       if (warp == kLead) {
         if (lane == 0 && wait(B_READY, it)) {
           tc::tc_fence_after();
-          constexpr uint32_t d1 = tc::instr_desc(tc::kFmtBF16, 128, 256, false, false);
+          constexpr uint32_t d1 = tc::instr_desc(tc::kFmtBF16, 128, 192, false, false);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             tc::mma_ss(0, tmem + TM_P, tc::smem_desc(sm + OFF_Q + ks * 32, 16, 1024),
                        tc::smem_desc(sm + OFF_K + ks * 32, 16, 1024), d1, ks > 0);
           tc::mma_commit(bars + B_M1);
-          ++m1;
+          ++begun[B_M1];
         }
         __syncwarp();
       }
     }
 
     // V1, V2 and V3: this thread's half of its token row, scaled and cut into 8-bit pieces
-    uint32_t third[16];
+    wait(B_V, it);
+    if (row >= L) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + OFF_V, zero);
+    }
     {
       const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? row + 1 : max(L - 1 - row, 0)));
       const f32x2 f = make2(f1, f1), half_ = make2(0.5f, 0.5f), mhalf = make2(-0.5f, -0.5f);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        uint32_t in[4], p1[4], p2[4];
+        uint32_t in[4], p1[4], p2[4], p3[4];
         lds128((at ^ (16 * x)) + OFF_V, in);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -287,22 +290,35 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
           p1[e] = high_halves(v);
           const f32x2 r = sub2(v, cut2(v));
           p2[e] = high_halves(r);
-          third[4 * x + e] = high_halves(fma2(cut2(r), mhalf, mul2(r, half_)));
+          p3[e] = high_halves(fma2(cut2(r), mhalf, mul2(r, half_)));
         }
         sts128((at ^ (16 * x)) + OFF_V1, p1);
         sts128((at ^ (16 * x)) + OFF_V2, p2);
+        sts128((at ^ (16 * x)) + OFF_V3, p3);
       }
     }
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bars + B_SPLIT);
+    if (warp == kLead) {
+      if (lane == 0 && wait(B_SPLIT, it)) {
+        tc::tc_fence_after();
+        constexpr uint32_t d3 = tc::instr_desc(tc::kFmtBF16, 128, 64, true, true);
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks)  // V1 over V2; then V3 over itself (block stride 0)
+          tc::mma_ss(0, tmem + TM_X,
+                     tc::smem_desc(sm + (ks < 8 ? OFF_V1 : OFF_V3) + (ks & 7) * 2048, ks < 8 ? kTile : 0, 1024),
+                     tc::smem_desc(sm + OFF_K + (ks & 7) * 2048, kTile, 1024), d3, ks > 0);
+        tc::mma_commit(bars + B_M3);
+        ++begun[B_M3];
+      }
+      __syncwarp();
+    }
+
     if (kOut) {
       wait(B_M1, it);
       tc::tc_fence_after();
-    }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const uint32_t p3[4] = {third[4 * x], third[4 * x + 1], third[4 * x + 2], third[4 * x + 3]};
-      sts128((at ^ (16 * x)) + OFF_Q, p3);
-    }
-    if (kOut) {
       // P: column groups half and half + 2, 32 columns each.  Both halves' warps have read their
       // products before either overwrites columns.
       float pk[2][16];
@@ -343,52 +359,42 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
       named_sync(1 + rb, 64);
       tc::tmem_st16(tml + TM_P + 16 * half, pk[0]);
       tc::tmem_st16(tml + TM_P + 16 * (half + 2), pk[1]);
-      // the state's part of the outputs, which MMA2 adds to
+      // the state's part of the outputs
       const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? max(L - 1 - row, 0) : row + 1));
       const f32x2 f = make2(f1, f1);
+      float y[32];
+      tc::tmem_ld32(tml + TM_Y + 32 * half, y);
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        float y[16], v[16];
-        tc::tmem_ld16(tml + TM_HI + 32 * half + 16 * n, y);
-        tc::tmem_ld16(tml + TM_LO + 32 * half + 16 * n, v);
-#pragma unroll
-        for (int x = 0; x < 16; x += 2)
-          split2(mul2(add2(make2(y[x], y[x + 1]), make2(v[x], v[x + 1])), f), y[x], y[x + 1]);
-        tc::tmem_st16(tml + TM_Y1 + 32 * half + 16 * n, y);
-      }
+      for (int x = 0; x < 32; x += 2) split2(mul2(make2(y[x], y[x + 1]), f), y[x], y[x + 1]);
+      tc::tmem_st32(tml + TM_Y + 32 * half, y);
       tc::tmem_st_wait();
       tc::tc_fence_before();
-    }
-    tc::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(bars + B_P);
-    if (warp == kLead) {
-      if (lane == 0 && wait(B_P, it)) {
-        tc::tc_fence_after();
-        constexpr uint32_t d2 = tc::instr_desc(tc::kFmtBF16, 128, 64, false, true);
-        constexpr uint32_t d3 = tc::instr_desc(tc::kFmtBF16, 128, 64, true, true);
-        if (kOut) {
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bars + B_P);
+      if (warp == kLead) {
+        if (lane == 0 && wait(B_P, it)) {
+          tc::tc_fence_after();
+          constexpr uint32_t d2 = tc::instr_desc(tc::kFmtBF16, 128, 64, false, true);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            tc::mma_ts_bf16(tmem + TM_Y1, tmem + TM_P + 8 * ks, tc::smem_desc(sm + OFF_V + ks * 2048, kTile, 1024), d2,
-                            1);
+            tc::mma_ts_bf16(tmem + TM_Y, tmem + TM_P + 8 * ks, tc::smem_desc(sm + OFF_V + ks * 2048, kTile, 1024), d2, 1);
+          tc::mma_commit(bars + B_M2);
+          ++begun[B_M2];
         }
-#pragma unroll
-        for (int ks = 0; ks < 16; ++ks)  // V1 over V2; then V3 over itself (block stride 0)
-          tc::mma_ss(0, tmem + TM_X,
-                     tc::smem_desc(sm + (ks < 8 ? OFF_V1 : OFF_Q) + (ks & 7) * 2048, ks < 8 ? kTile : 0, 1024),
-                     tc::smem_desc(sm + OFF_K + (ks & 7) * 2048, kTile, 1024), d3, ks > 0);
-        tc::mma_commit(bars + B_M2);
-        ++m2;
+        __syncwarp();
       }
-      __syncwarp();
     }
 
-    wait(B_M2, it);
+    // the state behind this chunk
+    wait(B_M3, it);
     tc::tc_fence_after();
     if (warp == kLead && lane == 0 && it + 1 < nchunks && !*bad) {
-      load_tiles(it + 1);
-      ++full;
+      load_qk(it + 1);
+      ++begun[B_QK];
+      if (!kOut) {
+        load_v(it + 1);
+        ++begun[B_V];
+      }
     }
     {
       float x32[32];
@@ -423,8 +429,14 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
     }
     if (kOut) {
       put_state();
+      wait(B_M2, it);
+      tc::tc_fence_after();
+      if (warp == kLead && lane == 0 && it + 1 < nchunks && !*bad) {
+        load_v(it + 1);
+        ++begun[B_V];
+      }
       float v[32];
-      tc::tmem_ld32(tml + TM_Y1 + 32 * half, v);
+      tc::tmem_ld32(tml + TM_Y + 32 * half, v);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         uint32_t u[4];
@@ -453,9 +465,8 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
   if (warp == kLead && lane == 0 && *bad) {
     // give up: whatever is still in flight lands first
     report_device_error(err_word, kDevErrTimeout);
-    if (full > 0) tc::mbar_wait_bounded(bars + B_FULL, (full - 1) & 1, kMaxPolls);
-    if (m1 > 0) tc::mbar_wait_bounded(bars + B_M1, (m1 - 1) & 1, kMaxPolls);
-    if (m2 > 0) tc::mbar_wait_bounded(bars + B_M2, (m2 - 1) & 1, kMaxPolls);
+    for (int k : {B_QK, B_V, B_M1, B_M3, B_M2})
+      if (begun[k] > 0) tc::mbar_wait_bounded(bars + k, (begun[k] - 1) & 1, kMaxPolls);
   }
   const bool ends = kRev ? sg.first : sg.last;
   float *to = !kOut ? A.ws + (pair * P.nseg + (kRev ? z - 1 : z + 1)) * (kN * kN)

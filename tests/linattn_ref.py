@@ -40,6 +40,24 @@ def products(q, k, v, w, reverse=False):
     return (((q @ k.transpose(-1, -2)) * D).abs() @ v.abs()).transpose(1, 2)
 
 
+def state_products(q, k, v, w, s0=None, reverse=False, C=128):
+    """What a rounding of the state that a chunk of C tokens begins with (reversed: of the one behind it) is
+    multiplied by: w^(tokens between) |S| |q_t|, summed over the 64 key channels."""
+    q, k, v, w = (x.double() for x in (q, k, v, w))
+    B, T, H, N = q.shape
+    out, S = torch.zeros_like(q), s0
+    starts = list(range(0, T, C))
+    for t0 in (reversed(starts) if reverse else starts):
+        n = min(C, T - t0)
+        part = [x[:, t0:t0 + n] for x in (q, k, v)]
+        if S is not None:
+            i = torch.arange(n, device=q.device, dtype=torch.float64)
+            f = torch.pow(w.view(1, 1, H, 1), ((n - 1 - i) if reverse else (i + 1)).view(1, n, 1, 1))
+            out[:, t0:t0 + n] = torch.einsum("bhij,bthj->bthi", S.double().abs(), part[0].abs()) * f
+        _, S = mix(*part, w, S, reverse)
+    return out
+
+
 def check_mix(out, s_end, q, k, v, w, s0=None, reverse=False, what=""):
     """out (its dtype says how it was rounded) and the end state (or None) of a pass against float64."""
     T = q.shape[1]
@@ -50,8 +68,10 @@ def check_mix(out, s_end, q, k, v, w, s0=None, reverse=False, what=""):
     if out is not None and T > 0:
         tol = n * mag
         if out.dtype == torch.bfloat16:
-            # the result's own rounding; the products' one; the state's second bf16 term, 2^-16 of it
-            tol = tol + BF16_HALF_STEP * (ref.abs() + products(q, k, v, w, reverse)) * (1 + 2.0 ** -6) + 2.0 ** -16 * mag
+            # the result's own rounding, the products' q_t . k_s one, and the one of the state that a chunk
+            # begins with: each moves its term by at most half a step, and nothing else is in bf16
+            tol = tol + BF16_HALF_STEP * (ref.abs() + products(q, k, v, w, reverse)
+                                          + state_products(q, k, v, w, s0, reverse)) * (1 + 2.0 ** -6)
         bad = ~((out.double() - ref).abs() <= tol + 1e-37)
         assert not bool(bad.any()), (what, "out", bad.nonzero()[:4].tolist(), float((out.double() - ref).abs().max()))
     if s_end is not None:

@@ -71,7 +71,9 @@ def test_prefill_state_in_place_and_chained(dtype):
     y1, s1 = lib7.linattn_prefill(*part[0], w, st)
     y2, s2 = lib7.linattn_prefill(*part[1], w, s1)
     done()
-    ref.check_mix(torch.cat([y1, y2], 1), s2, r, k, v, w, st)
+    ref.check_mix(y1, s1, *part[0], w, st)
+    ref.check_mix(y2, s2, *part[1], w, s1)
+    ref.check_mix(None, s2, r, k, v, w, st)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
