@@ -16,8 +16,9 @@
 // 32 (w % 4) .. + 31 and half w / 4 of their columns; the warp with the least to do in P also issues the
 // TMA loads and the MMAs.  Per chunk, float32 accumulation:
 //     MMA1  [128 x 192] = Q [K; S0]^T                K-major tiles, as TMA and the warps left them
-//     MMA2  [128 x 64] += P V                        P from TMEM in bf16, V as TMA left it (MN-major)
-//     MMA3  [128 x 64]  = [V1; V2] K, then + V3 K on both halves      (V1 + V2 + 2 V3 = w^(L-1-s) v_s)
+//     MMA2  [128 x 64]  = P V                        P from TMEM in bf16, V as TMA left it (MN-major)
+//     MMA3  [64 x 64]   = V1 K + V2 K + V3 K         V1 + V2 + V3 = w^(L-1-s) v_s, MN-major; run with 128 rows,
+//                                                    the 64 twice (block stride 0), so that every warp has a part
 // MMA3 and the new state run beside P and MMA2, and Q and K of the next chunk arrive meanwhile.
 // The state stays in float32 registers across chunks (16 elements per thread).  Roundings to bf16:
 //   P: one per product, as large as the rounding of out itself, and averaged over the tokens;
@@ -40,11 +41,11 @@ constexpr uint32_t kMaxPolls = 1u << 22;
 constexpr uint32_t kTile = kChunk * kN * 2;  // one bf16 128 x 64 tile, 128-byte swizzled rows
 
 // TMEM columns.  MMA1 fills 0 .. 191 (q k, then q S0); P (bf16 pairs) replaces the first 64 of the
-// products once they have been read; the state's part of out is scaled in place, and MMA2 adds to it.
-constexpr uint32_t TM_P = 0, TM_Y = 128, TM_X = 192, kTmemCols = 256;
+// products once they have been read, MMA2's result the second 64.
+constexpr uint32_t TM_P = 0, TM_Y = 64, TM_YS = 128, TM_X = 192, kTmemCols = 256;
 
-// shared memory, from a 1024-aligned base.  V1's tile is where the threads swap halves of MMA3's result
-// afterwards, V2's where they put the rows of out together.
+// shared memory, from a 1024-aligned base.  V1's tile is where the rows of out are put together for
+// their TMA store.
 constexpr uint32_t OFF_Q = 0, OFF_K = kTile;
 constexpr uint32_t OFF_S = 2 * kTile;  // [64 value channels][64 key channels]; MMA1's rows behind K
 constexpr uint32_t OFF_V = OFF_S + kN * kN * 2, OFF_V1 = OFF_V + kTile, OFF_V2 = OFF_V1 + kTile, OFF_V3 = OFF_V2 + kTile;
@@ -54,11 +55,11 @@ constexpr uint32_t OFF_PW = OFF_ZERO + 128;  // float [132]: w^n for n <= 128
 constexpr uint32_t OFF_PL = OFF_PW + 528;    // float [132]: what the rounding of w^n to float32 leaves
 constexpr uint32_t OFF_BAR = OFF_PL + 528;   // mbarriers, TMEM address, flags
 constexpr uint32_t kSmemBytes = OFF_BAR + 128 + 1024;
-// Tiles landed (Q and K; V); all warps ready for MMA1, MMA3, MMA2; each of those done.
-enum { B_QK, B_V, B_READY, B_SPLIT, B_P, B_M1, B_M3, B_M2, kBars };
+// Tiles landed (Q and K; V); all warps ready for MMA1, MMA3, MMA2; each of those done; V1's tile free again.
+enum { B_QK, B_V, B_READY, B_SPLIT, B_P, B_M1, B_M3, B_M2, B_OUT, kBars };
 
 struct Maps {
-  CUtensorMap q, k, v;  // [tokens, H, 64] bf16, box {64, 1, 128}
+  CUtensorMap q, k, v, out;  // [tokens, H, 64] bf16, box {64, 1, 128}
 };
 
 // two float32 values in a register pair, and the packed operations on them (one instruction each)
@@ -118,8 +119,24 @@ __device__ __forceinline__ float lds32(uint32_t p) {
   asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(p) : "memory");
   return v;
 }
+// true in one lane of the (converged) warp.  MMAs are issued under this predicate, in a branch that is
+// uniform for the warp: then an MMA takes 7 cycles to issue, under lane == 0 it takes 90 (measured
+// with 32 MMAs of 128 x 64 x 16, which take 50 each to run).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
 }
 
 template <bool kRev, bool kOut>
@@ -130,7 +147,8 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;  // shared-memory addresses from here on
   uint8_t *smem = smem_raw + (sm - smem_u32(smem_raw));
   const int h = blockIdx.x, b = blockIdx.y, z = blockIdx.z + (!kOut && kRev ? 1 : 0);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const bool elected = elect_one();
   pdl_wait();
   const Segment sg = segment(P, b, z);
   if (sg.len < 0) return;
@@ -144,26 +162,19 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
 
   const int nchunks = (sg.len + kChunk - 1) / kChunk;
   auto chunk_at = [&](int i) { return kRev ? nchunks - 1 - i : i; };
-  // Loads of chunk `it`, and the chunk after it on its way to L2.
   auto load_qk = [&](int it) {
-    const int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk, next = tok + (kRev ? -kChunk : kChunk);
+    const int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk;
     tc::mbar_arrive_expect_tx(bars + B_QK, (kOut ? 2 : 1) * kTile);
     tc::tma_load_3d(smem + OFF_K, &maps.k, bars + B_QK, 0, h, tok);
     if (kOut) tc::tma_load_3d(smem + OFF_Q, &maps.q, bars + B_QK, 0, h, tok);
-    if (it + 1 < nchunks) {
-      tc::tma_prefetch_l2_3d(&maps.k, 0, h, next);
-      if (kOut) tc::tma_prefetch_l2_3d(&maps.q, 0, h, next);
-    }
   };
   auto load_v = [&](int it) {
-    const int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk, next = tok + (kRev ? -kChunk : kChunk);
     tc::mbar_arrive_expect_tx(bars + B_V, kTile);
-    tc::tma_load_3d(smem + OFF_V, &maps.v, bars + B_V, 0, h, tok);
-    if (it + 1 < nchunks) tc::tma_prefetch_l2_3d(&maps.v, 0, h, next);
+    tc::tma_load_3d(smem + OFF_V, &maps.v, bars + B_V, 0, h, static_cast<int>(sg.lo) + chunk_at(it) * kChunk);
   };
   constexpr int kLead = kRev ? 3 : 4;  // its rows have no products, or one group of them
   if (warp == kLead) {
-    if (lane == 0) {
+    if (elected) {
       for (int i = 0; i < kBars; ++i) tc::mbar_init(bars + i, i >= B_READY && i <= B_P ? 8 : 1);
       tc::fence_mbar_init();
       *bad = 0;
@@ -194,11 +205,8 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
   const int row = 32 * rb + lane;
   // chunk x of this thread's half row of a swizzled tile is at tile + (at ^ 16 x)
   const uint32_t at = sm + row * 128u + (((4 * half) ^ (row & 7)) << 4);
-  // this thread's part of the state: row i (value channel), columns j0 .. j0 + 15.  Rows 0 .. 63 of MMA3's
-  // result are V1 K, rows 64 .. 127 V2 K: thread (row, half) sees columns 32 half .. + 31 of one of them,
-  // keeps 16 of those and swaps the others with thread (row ^ 64, half).
-  const bool upper = rb >= 2;
-  const int i = row & 63, j0 = 32 * half + (upper ? 16 : 0);
+  // this thread's part of the state: row i (value channel), columns j0 .. j0 + 15
+  const int i = row & 63, j0 = 32 * half + 16 * (row >> 6);
   const uint32_t at_s = sm + OFF_S + i * 128u + (((j0 >> 3) ^ (i & 7)) << 4);
   f32x2 S[8];
   auto put_state = [&]() {  // S in bf16, rows of MMA1's B operand
@@ -257,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bars + B_READY);
       if (warp == kLead) {
-        if (lane == 0 && wait(B_READY, it)) {
+        if (wait(B_READY, it) && elected) {
           tc::tc_fence_after();
           constexpr uint32_t d1 = tc::instr_desc(tc::kFmtBF16, 128, 192, false, false);
 #pragma unroll
@@ -266,6 +274,10 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
                        tc::smem_desc(sm + OFF_K + ks * 32, 16, 1024), d1, ks > 0);
           tc::mma_commit(bars + B_M1);
           ++begun[B_M1];
+        }
+        if (elected && it > 0) {
+          bulk_wait_read();
+          tc::mbar_arrive(bars + B_OUT);
         }
         __syncwarp();
       }
@@ -279,18 +291,19 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
     }
     {
       const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? row + 1 : max(L - 1 - row, 0)));
-      const f32x2 f = make2(f1, f1), half_ = make2(0.5f, 0.5f), mhalf = make2(-0.5f, -0.5f);
+      const f32x2 f = make2(f1, f1);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         uint32_t in[4], p1[4], p2[4], p3[4];
         lds128((at ^ (16 * x)) + OFF_V, in);
+        if (kOut && x == 0 && it > 0) wait(B_OUT, it - 1);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const f32x2 v = mul2(make2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), f);
           p1[e] = high_halves(v);
           const f32x2 r = sub2(v, cut2(v));
           p2[e] = high_halves(r);
-          p3[e] = high_halves(fma2(cut2(r), mhalf, mul2(r, half_)));
+          p3[e] = high_halves(sub2(r, cut2(r)));
         }
         sts128((at ^ (16 * x)) + OFF_V1, p1);
         sts128((at ^ (16 * x)) + OFF_V2, p2);
@@ -302,13 +315,12 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(bars + B_SPLIT);
     if (warp == kLead) {
-      if (lane == 0 && wait(B_SPLIT, it)) {
+      if (wait(B_SPLIT, it) && elected) {
         tc::tc_fence_after();
         constexpr uint32_t d3 = tc::instr_desc(tc::kFmtBF16, 128, 64, true, true);
 #pragma unroll
-        for (int ks = 0; ks < 16; ++ks)  // V1 over V2; then V3 over itself (block stride 0)
-          tc::mma_ss(0, tmem + TM_X,
-                     tc::smem_desc(sm + (ks < 8 ? OFF_V1 : OFF_V3) + (ks & 7) * 2048, ks < 8 ? kTile : 0, 1024),
+        for (int ks = 0; ks < 24; ++ks)
+          tc::mma_ss(0, tmem + TM_X, tc::smem_desc(sm + OFF_V1 + ks * 2048, 0, 1024),
                      tc::smem_desc(sm + OFF_K + (ks & 7) * 2048, kTile, 1024), d3, ks > 0);
         tc::mma_commit(bars + B_M3);
         ++begun[B_M3];
@@ -359,25 +371,18 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
       named_sync(1 + rb, 64);
       tc::tmem_st16(tml + TM_P + 16 * half, pk[0]);
       tc::tmem_st16(tml + TM_P + 16 * (half + 2), pk[1]);
-      // the state's part of the outputs
-      const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? max(L - 1 - row, 0) : row + 1));
-      const f32x2 f = make2(f1, f1);
-      float y[32];
-      tc::tmem_ld32(tml + TM_Y + 32 * half, y);
-#pragma unroll
-      for (int x = 0; x < 32; x += 2) split2(mul2(make2(y[x], y[x + 1]), f), y[x], y[x + 1]);
-      tc::tmem_st32(tml + TM_Y + 32 * half, y);
       tc::tmem_st_wait();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bars + B_P);
       if (warp == kLead) {
-        if (lane == 0 && wait(B_P, it)) {
+        if (wait(B_P, it) && elected) {
           tc::tc_fence_after();
           constexpr uint32_t d2 = tc::instr_desc(tc::kFmtBF16, 128, 64, false, true);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            tc::mma_ts_bf16(tmem + TM_Y, tmem + TM_P + 8 * ks, tc::smem_desc(sm + OFF_V + ks * 2048, kTile, 1024), d2, 1);
+            tc::mma_ts_bf16(tmem + TM_Y, tmem + TM_P + 8 * ks, tc::smem_desc(sm + OFF_V + ks * 2048, kTile, 1024), d2,
+                            ks > 0);
           tc::mma_commit(bars + B_M2);
           ++begun[B_M2];
         }
@@ -388,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
     // the state behind this chunk
     wait(B_M3, it);
     tc::tc_fence_after();
-    if (warp == kLead && lane == 0 && it + 1 < nchunks && !*bad) {
+    if (warp == kLead && elected && it + 1 < nchunks && !*bad) {
       load_qk(it + 1);
       ++begun[B_QK];
       if (!kOut) {
@@ -397,72 +402,61 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
       }
     }
     {
-      float x32[32];
-      tc::tmem_ld32(tml + TM_X + 32 * half, x32);
-      f32x2 mine[8];
-      // (the same for a whole warp)
-      if (upper) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sts128f((at ^ (16 * x)) + OFF_V1, x32 + 4 * x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mine[e] = make2(x32[16 + 2 * e], x32[17 + 2 * e]);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sts128f((at ^ (16 * x)) + OFF_V1, x32 + 16 + 4 * x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mine[e] = make2(x32[2 * e], x32[1 + 2 * e]);
-      }
-      named_sync(5 + 2 * half + (rb & 1), 64);
+      float x16[16];
+      tc::tmem_ld16(tml + TM_X + j0, x16);
       const float f1 = lds32(sm + OFF_PW + 4 * L), f2 = lds32(sm + OFF_PL + 4 * L);
       const f32x2 f = make2(f1, f1), fl = make2(f2, f2);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint32_t u[4];
-        lds128((at ^ (16 * x)) + OFF_V1 + (upper ? -64 * 128 : 64 * 128), u);  // row ^ 64
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const f32x2 o = make2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
-          f32x2 &s = S[2 * x + e];
-          s = fma2(s, f, fma2(s, fl, add2(mine[2 * x + e], o)));
-        }
-      }
+      for (int e = 0; e < 8; ++e) S[e] = fma2(S[e], f, fma2(S[e], fl, make2(x16[2 * e], x16[2 * e + 1])));
     }
     if (kOut) {
       put_state();
+      // out: the state's part and that of the chunk's own tokens
+      const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? max(L - 1 - row, 0) : row + 1));
+      const f32x2 f = make2(f1, f1);
+      float y[32], v[32];
+      tc::tmem_ld32(tml + TM_YS + 32 * half, y);
       wait(B_M2, it);
       tc::tc_fence_after();
-      if (warp == kLead && lane == 0 && it + 1 < nchunks && !*bad) {
+      if (warp == kLead && elected && it + 1 < nchunks && !*bad) {
         load_v(it + 1);
         ++begun[B_V];
       }
-      float v[32];
       tc::tmem_ld32(tml + TM_Y + 32 * half, v);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         uint32_t u[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = pack2(make2(v[8 * x + 2 * e], v[8 * x + 2 * e + 1]));
-        sts128((at ^ (16 * x)) + OFF_V2, u);
+        for (int e = 0; e < 4; ++e)
+          u[e] = pack2(fma2(make2(y[8 * x + 2 * e], y[8 * x + 2 * e + 1]), f, make2(v[8 * x + 2 * e], v[8 * x + 2 * e + 1])));
+        sts128((at ^ (16 * x)) + OFF_V1, u);
       }
-      __syncwarp();
-      // the warp's 32 half rows, 4 lanes to each: rows r0, r0 + 8, ..
-      const int r0 = 32 * rb + (lane >> 2), ch = 4 * half + (lane & 3);
-      uint16_t *out = A.out + ((sg.lo + c * kChunk + r0) * P.H + h) * kN + 8 * ch;
-      const uint32_t from = sm + OFF_V2 + r0 * 128 + ((ch ^ (r0 & 7)) << 4);
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        uint32_t u[4];
-        lds128(from + 1024 * n, u);
-        if (r0 + 8 * n < L)
+      if (L == kChunk) {
+        tc::fence_proxy_async_smem();
+      } else {
+        // not the whole tile: the warp's 32 half rows, 4 lanes to each
+        __syncwarp();
+        const int r0 = 32 * rb + (lane >> 2), ch = 4 * half + (lane & 3);
+        uint16_t *out = A.out + ((sg.lo + c * kChunk + r0) * P.H + h) * kN + 8 * ch;
+        const uint32_t from = sm + OFF_V1 + r0 * 128 + ((ch ^ (r0 & 7)) << 4);
+        for (int n = 0; r0 + 8 * n < L && n < 4; ++n) {
+          uint32_t u[4];
+          lds128(from + 1024 * n, u);
           *reinterpret_cast<uint4 *>(out + static_cast<long long>(8 * n) * P.H * kN) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
       }
     }
     tc::tc_fence_before();
     if (tid == 0) *stop = *bad;
-    named_sync(9, kThreads);
+    named_sync(5, kThreads);
     if (*stop) break;
+    if (kOut && L == kChunk && warp == kLead && elected) {
+      tma_store_3d(&maps.out, sm + OFF_V1, 0, h, static_cast<int>(sg.lo) + c * kChunk);
+      tc::bulk_commit_group();
+    }
   }
-  if (warp == kLead && lane == 0 && *bad) {
+  if (kOut && warp == kLead && elected) tc::bulk_wait_all();
+  if (warp == kLead && elected && *bad) {
     // give up: whatever is still in flight lands first
     report_device_error(err_word, kDevErrTimeout);
     for (int k : {B_QK, B_V, B_M1, B_M3, B_M2})
@@ -525,9 +519,10 @@ cudaError_t launch_linattn_chunk(const lin::Pass<uint16_t> &A, const lin::Shape 
   const int nz = A.state_only ? P.nseg - 1 : P.nseg;
   if (nz <= 0) return cudaSuccess;
   Maps maps;
-  // a call for the states alone loads no q: any valid map does
+  // a call for the states alone loads no q and stores no out: any valid map does
   if (!make_map(&maps.k, A.k, P.total_T, P.H) || !make_map(&maps.v, A.v, P.total_T, P.H) ||
-      !make_map(&maps.q, A.state_only ? A.k : A.q, P.total_T, P.H))
+      !make_map(&maps.q, A.state_only ? A.k : A.q, P.total_T, P.H) ||
+      !make_map(&maps.out, A.state_only ? A.k : A.out, P.total_T, P.H))
     return cudaErrorInvalidValue;
   auto run = [&](auto kern) -> cudaError_t {
     const cudaError_t e =
