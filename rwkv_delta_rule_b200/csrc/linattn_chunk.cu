@@ -17,8 +17,7 @@
 // TMA loads and the MMAs.  Per chunk, float32 accumulation:
 //     MMA1  [128 x 192] = Q [K; S0]^T                K-major tiles, as TMA and the warps left them
 //     MMA2  [128 x 64]  = P V                        P from TMEM in bf16, V as TMA left it (MN-major)
-//     MMA3  [64 x 64]   = V1 K + V2 K + V3 K         V1 + V2 + V3 = w^(L-1-s) v_s, MN-major; run with 128 rows,
-//                                                    the 64 twice (block stride 0), so that every warp has a part
+//     MMA3  [64 x 64]   = V1 K + V2 K + V3 K         V1 + V2 + V3 = w^(L-1-s) v_s, MN-major
 // MMA3 and the new state run beside P and MMA2, and Q and K of the next chunk arrive meanwhile.
 // The state stays in float32 registers across chunks (16 elements per thread).  Roundings to bf16:
 //   P: one per product, as large as the rounding of out itself, and averaged over the tokens;
@@ -41,7 +40,7 @@ constexpr uint32_t kMaxPolls = 1u << 22;
 constexpr uint32_t kTile = kChunk * kN * 2;  // one bf16 128 x 64 tile, 128-byte swizzled rows
 
 // TMEM columns.  MMA1 fills 0 .. 191 (q k, then q S0); P (bf16 pairs) replaces the first 64 of the
-// products once they have been read, MMA2's result the second 64.
+// products once they have been read, MMA2's result the second 64.  MMA3's 64 rows lie 16 to each warp's 32 lanes.
 constexpr uint32_t TM_P = 0, TM_Y = 64, TM_YS = 128, TM_X = 192, kTmemCols = 256;
 
 // shared memory, from a 1024-aligned base.  V1's tile is where the rows of out are put together for
@@ -106,9 +105,8 @@ __device__ __forceinline__ void sts128(uint32_t p, const uint32_t (&u)[4]) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
                : "memory");
 }
-__device__ __forceinline__ void sts128f(uint32_t p, const float *u) {
-  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(p), "f"(u[0]), "f"(u[1]), "f"(u[2]), "f"(u[3])
-               : "memory");
+__device__ __forceinline__ void sts32(uint32_t p, uint32_t u) {
+  asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(p), "r"(u) : "memory");
 }
 __device__ __forceinline__ void lds128(uint32_t p, uint32_t (&u)[4]) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(p)
@@ -118,6 +116,20 @@ __device__ __forceinline__ float lds32(uint32_t p) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];\n" : "=f"(v) : "r"(p) : "memory");
   return v;
+}
+// 16 lanes x 32 columns of 32-bit, spread over the warp: pair 2 n + u of a thread is lane t / 4 + 8 u,
+// columns 8 n + 2 (t % 4), + 1.  Load followed by the wait.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, f32x2 (&v)[8]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = make2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
 }
 // true in one lane of the (converged) warp.  MMAs are issued under this predicate, in a branch that is
 // uniform for the warp: then an MMA takes 7 cycles to issue, under lane == 0 it takes 90 (measured
@@ -162,15 +174,22 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
 
   const int nchunks = (sg.len + kChunk - 1) / kChunk;
   auto chunk_at = [&](int i) { return kRev ? nchunks - 1 - i : i; };
+  // loads of chunk `it`, and the chunk after it on its way to L2
   auto load_qk = [&](int it) {
-    const int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk;
+    const int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk, next = tok + (kRev ? -kChunk : kChunk);
     tc::mbar_arrive_expect_tx(bars + B_QK, (kOut ? 2 : 1) * kTile);
     tc::tma_load_3d(smem + OFF_K, &maps.k, bars + B_QK, 0, h, tok);
     if (kOut) tc::tma_load_3d(smem + OFF_Q, &maps.q, bars + B_QK, 0, h, tok);
+    if (it + 1 < nchunks) {
+      tc::tma_prefetch_l2_3d(&maps.k, 0, h, next);
+      if (kOut) tc::tma_prefetch_l2_3d(&maps.q, 0, h, next);
+    }
   };
   auto load_v = [&](int it) {
+    const int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk, next = tok + (kRev ? -kChunk : kChunk);
     tc::mbar_arrive_expect_tx(bars + B_V, kTile);
-    tc::tma_load_3d(smem + OFF_V, &maps.v, bars + B_V, 0, h, static_cast<int>(sg.lo) + chunk_at(it) * kChunk);
+    tc::tma_load_3d(smem + OFF_V, &maps.v, bars + B_V, 0, h, tok);
+    if (it + 1 < nchunks) tc::tma_prefetch_l2_3d(&maps.v, 0, h, next);
   };
   constexpr int kLead = kRev ? 3 : 4;  // its rows have no products, or one group of them
   if (warp == kLead) {
@@ -205,18 +224,14 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
   const int row = 32 * rb + lane;
   // chunk x of this thread's half row of a swizzled tile is at tile + (at ^ 16 x)
   const uint32_t at = sm + row * 128u + (((4 * half) ^ (row & 7)) << 4);
-  // this thread's part of the state: row i (value channel), columns j0 .. j0 + 15
-  const int i = row & 63, j0 = 32 * half + 16 * (row >> 6);
-  const uint32_t at_s = sm + OFF_S + i * 128u + (((j0 >> 3) ^ (i & 7)) << 4);
+  // this thread's part of the state, as MMA3's result is read: pair 2 n + u is row (value channel)
+  // i0 + 8 u, columns j0 + 8 n, + 1
+  const int i0 = 16 * rb + (lane >> 2), j0 = 32 * half + 2 * (lane & 3);
+  const uint32_t at_s = sm + OFF_S + i0 * 128u + 4 * (lane & 3) + (((4 * half) ^ (lane >> 2)) << 4);
   f32x2 S[8];
   auto put_state = [&]() {  // S in bf16, rows of MMA1's B operand
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t u[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = pack2(S[4 * c + e]);
-      sts128(at_s ^ (16 * c), u);
-    }
+    for (int e = 0; e < 8; ++e) sts32((at_s ^ (16 * (e >> 1))) + 1024 * (e & 1), pack2(S[e]));
   };
   {
     const float *from = !kOut ? nullptr : P.nseg > 1 ? A.ws + (pair * P.nseg + z) * (kN * kN) : A.s_in;
@@ -225,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       S[e] = from == nullptr ? make2(0.f, 0.f)
-                             : make2(from[state_at(t, i, j0 + 2 * e)], from[state_at(t, i, j0 + 2 * e + 1)]);
+                             : make2(from[state_at(t, i0 + 8 * (e & 1), j0 + 8 * (e >> 1))],
+                                     from[state_at(t, i0 + 8 * (e & 1), j0 + 8 * (e >> 1) + 1)]);
     if (kOut) put_state();
   }
   tc::tc_fence_before();
@@ -317,10 +333,10 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
     if (warp == kLead) {
       if (wait(B_SPLIT, it) && elected) {
         tc::tc_fence_after();
-        constexpr uint32_t d3 = tc::instr_desc(tc::kFmtBF16, 128, 64, true, true);
+        constexpr uint32_t d3 = tc::instr_desc(tc::kFmtBF16, 64, 64, true, true);
 #pragma unroll
         for (int ks = 0; ks < 24; ++ks)
-          tc::mma_ss(0, tmem + TM_X, tc::smem_desc(sm + OFF_V1 + ks * 2048, 0, 1024),
+          tc::mma_ss(0, tmem + TM_X, tc::smem_desc(sm + OFF_V1 + ks * 2048, kTile, 1024),
                      tc::smem_desc(sm + OFF_K + (ks & 7) * 2048, kTile, 1024), d3, ks > 0);
         tc::mma_commit(bars + B_M3);
         ++begun[B_M3];
@@ -402,12 +418,12 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
       }
     }
     {
-      float x16[16];
-      tc::tmem_ld16(tml + TM_X + j0, x16);
+      f32x2 x[8];
+      tmem_ld_16x32(tml + TM_X + 32 * half, x);
       const float f1 = lds32(sm + OFF_PW + 4 * L), f2 = lds32(sm + OFF_PL + 4 * L);
       const f32x2 f = make2(f1, f1), fl = make2(f2, f2);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) S[e] = fma2(S[e], f, fma2(S[e], fl, make2(x16[2 * e], x16[2 * e + 1])));
+      for (int e = 0; e < 8; ++e) S[e] = fma2(S[e], f, fma2(S[e], fl, x[e]));
     }
     if (kOut) {
       put_state();
@@ -470,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
     for (int e = 0; e < 8; ++e) {
       float x, y;
       split2(S[e], x, y);
-      to[state_at(kOut && A.s_out_t, i, j0 + 2 * e)] = x;
-      to[state_at(kOut && A.s_out_t, i, j0 + 2 * e + 1)] = y;
+      to[state_at(kOut && A.s_out_t, i0 + 8 * (e & 1), j0 + 8 * (e >> 1))] = x;
+      to[state_at(kOut && A.s_out_t, i0 + 8 * (e & 1), j0 + 8 * (e >> 1) + 1)] = y;
     }
   }
   tc::tc_fence_before();
