@@ -18,7 +18,12 @@ template <typename TIn> struct Pass {
   int s_in_t, s_out_t;   // the state is stored transposed there
   float *ws;             // nseg > 1: [B, H, nseg, 64, 64], slot z is the state that segment z begins with
   int reverse;
-  int state_only;        // no outputs: what each segment adds to the state, for the segment after it (q, out unused)
+};
+// Passes over operands of one shape that run side by side (the backward has three).
+template <typename TIn> struct Passes {
+  Pass<TIn> p[3];
+  int n;
+  int state_only;  // no outputs: what each segment adds to the state, for the segment after it (q, out unused)
 };
 
 struct Shape {
@@ -71,14 +76,14 @@ __device__ __forceinline__ int state_at(int transposed, int row, int col) {
 
 // Launchers of the passes; TIn: float or uint16_t (bfloat16 bits).
 template <typename TIn>
-cudaError_t launch_linattn_scan(const lin::Pass<TIn> &pass, const lin::Shape &shape, int B, cudaStream_t stream);
-// A pass with state_only leaves what each segment adds to the state in the slot of the segment
+cudaError_t launch_linattn_scan(const lin::Passes<TIn> &passes, const lin::Shape &shape, int B, cudaStream_t stream);
+// Passes with state_only leave what each segment adds to the state in the slot of the segment
 // after it.  This turns the slots into the states that the segments begin with; the segments read
 // only those, so s_in may be s_out.
 template <typename TIn>
-cudaError_t launch_linattn_join(const lin::Pass<TIn> &pass, const lin::Shape &shape, int B, cudaStream_t stream);
-// The same pass on the tensor cores (linattn_chunk.cu); total_T > 0.  err_word: where its bounded waits report.
-cudaError_t launch_linattn_chunk(const lin::Pass<uint16_t> &pass, const lin::Shape &shape, int B, int *err_word,
+cudaError_t launch_linattn_join(const lin::Passes<TIn> &passes, const lin::Shape &shape, int B, cudaStream_t stream);
+// The same on the tensor cores (linattn_chunk.cu); total_T > 0.  err_word: where its bounded waits report.
+cudaError_t launch_linattn_chunk(const lin::Passes<uint16_t> &passes, const lin::Shape &shape, int B, int *err_word,
                                  cudaStream_t stream);
 template <typename TIn>
 cudaError_t launch_linattn_decode(const TIn *r, const TIn *k, const TIn *v, const float *w, float *s, TIn *y, int B,

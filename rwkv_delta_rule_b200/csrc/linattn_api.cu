@@ -20,21 +20,29 @@ constexpr long long kStateBytes = kN * kN * sizeof(float);
 constexpr long long kChunkMinT = 32;
 template <typename TIn> bool use_chunk(long long max_T) { return sizeof(TIn) == 2 && max_T >= kChunkMinT; }
 
-// Segments a sequence of at most T tokens is split into, for `pairs` chains: as many as fill the CTAs
-// that the device runs at once (2 per SM on the tensor cores, 4 of the token-by-token kernel).
-int segments(long long pairs, long long T, bool chunk) {
-  const long long want = (chunk ? 296 : 592) / pairs, most = T / 128;
+// Segments a sequence of at most T tokens is split into, for `chains` sequences that run side by side: as
+// many as fill the CTAs that the device runs at once (2 per SM on the tensor cores, 4 of the
+// token-by-token kernel).
+int segments(long long chains, long long T, bool chunk) {
+  const long long want = (chunk ? 296 : 592) / chains, most = T / 128;
   const long long n = want < most ? want : most;
   return n < 1 ? 1 : static_cast<int>(n);
 }
 // Workspace of one pass: a state per segment and pair where there is more than one segment.
 long long pass_bytes(long long pairs, int nseg) { return nseg > 1 ? pairs * nseg * kStateBytes : 0; }
 
+long long workspace(int B, int max_T, int H, int passes) {
+  if (B <= 0 || H <= 0 || max_T <= 0) return 0;
+  const long long pairs = static_cast<long long>(B) * H;
+  const int a = segments(passes * pairs, max_T, false), b = segments(passes * pairs, max_T, true);
+  return passes * pass_bytes(pairs, a > b ? a : b);
+}
+
 // Splits for the workspace given: fewer segments where it holds no more.
 lin::Shape shape(const float *w, const int32_t *cu, int B, int T, long long total_T, long long max_T, int H,
                  long long bytes, int passes, bool chunk) {
   const long long pairs = static_cast<long long>(B) * H;
-  int n = segments(pairs, max_T, chunk);
+  int n = segments(passes * pairs, max_T, chunk);
   const long long room = bytes / (passes * pairs * kStateBytes);
   if (n > room) n = room < 2 ? 1 : static_cast<int>(room);
   const long long len = (((max_T + n - 1) / n) + 127) / 128 * 128;
@@ -42,24 +50,24 @@ lin::Shape shape(const float *w, const int32_t *cu, int B, int T, long long tota
   return lin::Shape{w, cu, T, total_T, H, n, n > 1 ? static_cast<int>(len) : 0x7fffff80};
 }
 
-template <typename TIn> cudaError_t one_pass(const lin::Pass<TIn> &p, const lin::Shape &s, int B, bool chunk,
-                                             cudaStream_t stream) {
+template <typename TIn> cudaError_t one_sweep(const lin::Passes<TIn> &p, const lin::Shape &s, int B, bool chunk,
+                                              cudaStream_t stream) {
   if constexpr (sizeof(TIn) == 2) {
     if (chunk) return launch_linattn_chunk(p, s, B, device_error_word(), stream);
   }
   return launch_linattn_scan(p, s, B, stream);
 }
 
-template <typename TIn> cudaError_t run_pass(lin::Pass<TIn> p, const lin::Shape &s, int B, bool chunk,
-                                             cudaStream_t stream) {
+template <typename TIn> cudaError_t run_passes(const lin::Passes<TIn> &p, const lin::Shape &s, int B, bool chunk,
+                                               cudaStream_t stream) {
   if (s.nseg > 1) {
-    lin::Pass<TIn> own = p;
-    own.state_only = 1;
-    cudaError_t e = one_pass(own, s, B, chunk, stream);
-    if (e == cudaSuccess) e = launch_linattn_join(own, s, B, stream);
+    lin::Passes<TIn> states = p;
+    states.state_only = 1;
+    cudaError_t e = one_sweep(states, s, B, chunk, stream);
+    if (e == cudaSuccess) e = launch_linattn_join(states, s, B, stream);
     if (e != cudaSuccess) return e;
   }
-  return one_pass(p, s, B, chunk, stream);
+  return one_sweep(p, s, B, chunk, stream);
 }
 
 template <typename TIn>
@@ -82,8 +90,8 @@ rwkv7_status prefill(int B, int T, long long total_T, long long max_T, int H, in
   if (st != RWKV7_OK) return st;
   const bool chunk = use_chunk<TIn>(max_T) && total_T > 0;
   const lin::Shape s = shape(w, cu, B, T, total_T, max_T, H, ws_bytes, 1, chunk);
-  const lin::Pass<TIn> p{r, k, v, y, s_in, s_out, 0, 0, static_cast<float *>(ws), 0, 0};
-  return from_cuda(run_pass(p, s, B, chunk, reinterpret_cast<cudaStream_t>(stream)));
+  const lin::Passes<TIn> p{{{r, k, v, y, s_in, s_out, 0, 0, static_cast<float *>(ws), 0}}, 1, 0};
+  return from_cuda(run_passes(p, s, B, chunk, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 template <typename TIn>
@@ -130,14 +138,9 @@ using namespace rwkv7;
 
 extern "C" {
 
-long long rwkv7_linattn_workspace(int B, int max_T, int H) {
-  if (B <= 0 || H <= 0 || max_T <= 0) return 0;
-  const long long pairs = static_cast<long long>(B) * H;
-  const int a = segments(pairs, max_T, false), b = segments(pairs, max_T, true);
-  return pass_bytes(pairs, a > b ? a : b);
-}
+long long rwkv7_linattn_workspace(int B, int max_T, int H) { return workspace(B, max_T, H, 1); }
 
-long long rwkv7_linattn_backward_workspace(int B, int T, int H) { return 3 * rwkv7_linattn_workspace(B, T, H); }
+long long rwkv7_linattn_backward_workspace(int B, int T, int H) { return workspace(B, T, H, 3); }
 
 rwkv7_status rwkv7_linattn_prefill(int B, int T, int H, int N, const float *r, const float *k, const float *v,
                                    const float *w, const float *s_in, float *y, float *s_out, void *workspace,
@@ -199,16 +202,20 @@ rwkv7_status rwkv7_linattn_backward_bf16(int B, int T, int H, int N, const uint1
   const lin::Shape s = shape(w, nullptr, B, T, tokens, T, H, workspace_bytes, 3, chunk);
   float *ws = static_cast<float *>(workspace);
   const long long part = s.nseg > 1 ? static_cast<long long>(B) * H * s.nseg * kN * kN : 0;
-  const lin::Pass<uint16_t> passes[3] = {
-      {dy, v, k, dr, s_in, nullptr, 1, 0, ws, 0, 0},
-      {v, dy, r, dk, ds_out, nullptr, 1, 0, ws + part, 1, 0},
-      {k, r, dy, dv, ds_out, ds_in, 0, 0, ws + 2 * part, 1, 0},
-  };
-  for (const lin::Pass<uint16_t> &p : passes) {
-    const cudaError_t e = run_pass(p, s, B, chunk, cs);
-    if (e != cudaSuccess) return RWKV7_ERR_CUDA;
+  const lin::Passes<uint16_t> p{{{dy, v, k, dr, s_in, nullptr, 1, 0, ws, 0},
+                                 {v, dy, r, dk, ds_out, nullptr, 1, 0, ws + part, 1},
+                                 {k, r, dy, dv, ds_out, ds_in, 0, 0, ws + 2 * part, 1}},
+                                3, 0};
+  if (ds_in != nullptr && ds_in == ds_out && s.nseg == 1) {
+    // in place, and no workspace that holds ds_out meanwhile: the pass that writes it goes last
+    lin::Passes<uint16_t> first = p, last = p;
+    first.n = 2;
+    last.n = 1;
+    last.p[0] = p.p[2];
+    const cudaError_t e = run_passes(first, s, B, chunk, cs);
+    return from_cuda(e != cudaSuccess ? e : run_passes(last, s, B, chunk, cs));
   }
-  return RWKV7_OK;
+  return from_cuda(run_passes(p, s, B, chunk, cs));
 }
 
 long long rwkv7_layer_norm_workspace(int bf16, int M, int G, int D) {

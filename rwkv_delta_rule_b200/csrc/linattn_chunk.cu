@@ -151,17 +151,15 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t sr
                : "memory");
 }
 
+// One segment of one pass.
 template <bool kRev, bool kOut>
-__global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid_constant__ Maps maps,
-                                                                    const Pass<uint16_t> A, const Shape P,
-                                                                    int *err_word) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
+__device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, const Shape &P, int z,
+                                     uint8_t *smem_raw, int *err_word) {
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;  // shared-memory addresses from here on
   uint8_t *smem = smem_raw + (sm - smem_u32(smem_raw));
-  const int h = blockIdx.x, b = blockIdx.y, z = blockIdx.z + (!kOut && kRev ? 1 : 0);
+  const int h = blockIdx.x, b = blockIdx.y;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool elected = elect_one();
-  pdl_wait();
   const Segment sg = segment(P, b, z);
   if (sg.len < 0) return;
   if (!kOut && (kRev ? sg.first : sg.last)) return;
@@ -308,23 +306,25 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
     {
       const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? row + 1 : max(L - 1 - row, 0)));
       const f32x2 f = make2(f1, f1);
+      uint32_t p1[4][4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        uint32_t in[4], p1[4], p2[4], p3[4];
+        uint32_t in[4], p2[4], p3[4];
         lds128((at ^ (16 * x)) + OFF_V, in);
-        if (kOut && x == 0 && it > 0) wait(B_OUT, it - 1);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const f32x2 v = mul2(make2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), f);
-          p1[e] = high_halves(v);
+          p1[x][e] = high_halves(v);
           const f32x2 r = sub2(v, cut2(v));
           p2[e] = high_halves(r);
           p3[e] = high_halves(sub2(r, cut2(r)));
         }
-        sts128((at ^ (16 * x)) + OFF_V1, p1);
         sts128((at ^ (16 * x)) + OFF_V2, p2);
         sts128((at ^ (16 * x)) + OFF_V3, p3);
       }
+      if (kOut && it > 0) wait(B_OUT, it - 1);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + OFF_V1, p1[x]);
     }
     tc::fence_proxy_async_smem();
     tc::tc_fence_before();
@@ -498,6 +498,25 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
   }
 }
 
+struct AllMaps {
+  Maps m[3];
+};
+
+// blockIdx = (head, batch row, pass and segment); the passes for the states alone leave out the segment
+// that none continues from.
+template <bool kOut>
+__global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid_constant__ AllMaps maps,
+                                                                    const __grid_constant__ Passes<uint16_t> A,
+                                                                    const Shape P, int *err_word) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  pdl_wait();
+  const int nz = kOut ? P.nseg : P.nseg - 1, role = blockIdx.z / nz, z = blockIdx.z - role * nz;
+  if (A.p[role].reverse)
+    walk<true, kOut>(maps.m[role], A.p[role], P, kOut ? z : z + 1, smem_raw, err_word);
+  else
+    walk<false, kOut>(maps.m[role], A.p[role], P, z, smem_raw, err_word);
+}
+
 using PFN_encodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                      const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
                                      CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
@@ -529,26 +548,29 @@ static bool make_map(CUtensorMap *map, const void *base, long long tokens, int H
 
 }  // namespace lin
 
-cudaError_t launch_linattn_chunk(const lin::Pass<uint16_t> &A, const lin::Shape &P, int B, int *err_word,
+cudaError_t launch_linattn_chunk(const lin::Passes<uint16_t> &A, const lin::Shape &P, int B, int *err_word,
                                  cudaStream_t stream) {
   using namespace lin;
   const int nz = A.state_only ? P.nseg - 1 : P.nseg;
   if (nz <= 0) return cudaSuccess;
-  Maps maps;
-  // a call for the states alone loads no q and stores no out: any valid map does
-  if (!make_map(&maps.k, A.k, P.total_T, P.H) || !make_map(&maps.v, A.v, P.total_T, P.H) ||
-      !make_map(&maps.q, A.state_only ? A.k : A.q, P.total_T, P.H) ||
-      !make_map(&maps.out, A.state_only ? A.k : A.out, P.total_T, P.H))
-    return cudaErrorInvalidValue;
+  AllMaps maps;
+  for (int i = 0; i < A.n; ++i) {
+    const Pass<uint16_t> &p = A.p[i];
+    Maps &m = maps.m[i];
+    // a call for the states alone loads no q and stores no out: any valid map does
+    if (!make_map(&m.k, p.k, P.total_T, P.H) || !make_map(&m.v, p.v, P.total_T, P.H) ||
+        !make_map(&m.q, A.state_only ? p.k : p.q, P.total_T, P.H) ||
+        !make_map(&m.out, A.state_only ? p.k : p.out, P.total_T, P.H))
+      return cudaErrorInvalidValue;
+  }
   auto run = [&](auto kern) -> cudaError_t {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
     if (e != cudaSuccess) return e;
-    kern<<<dim3(P.H, B, nz), kThreads, kSmemBytes, stream>>>(maps, A, P, err_word);
+    kern<<<dim3(P.H, B, nz * A.n), kThreads, kSmemBytes, stream>>>(maps, A, P, err_word);
     return cudaGetLastError();
   };
-  if (A.state_only) return A.reverse ? run(linattn_chunk_kernel<true, false>) : run(linattn_chunk_kernel<false, false>);
-  return A.reverse ? run(linattn_chunk_kernel<true, true>) : run(linattn_chunk_kernel<false, true>);
+  return A.state_only ? run(linattn_chunk_kernel<false>) : run(linattn_chunk_kernel<true>);
 }
 
 }  // namespace rwkv7

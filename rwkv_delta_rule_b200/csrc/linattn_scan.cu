@@ -32,15 +32,11 @@ __device__ __forceinline__ void stage(const Pass<TIn> &A, TIn *buf, long long to
 }
 
 template <typename TIn, bool kRev, bool kOut>
-__global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const Pass<TIn> A, const Shape P) {
+__device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P, int z, uint8_t *smem_raw) {
   using C = Tile<TIn>;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
   TIn *bufs = reinterpret_cast<TIn *>(smem_raw);
   float *ys = reinterpret_cast<float *>(smem_raw + 2 * C::kElems * sizeof(TIn));
   const int h = blockIdx.x, b = blockIdx.y;
-  // the state pass covers the segments that another one continues from
-  const int z = blockIdx.z + (!kOut && kRev ? 1 : 0);
-  pdl_wait();
   const Segment sg = segment(P, b, z);
   if (sg.len < 0) return;
   if (!kOut && (kRev ? sg.first : sg.last)) return;
@@ -140,16 +136,31 @@ __global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const Pass<TIn> 
   }
 }
 
+// blockIdx = (head, batch row, pass and segment); the passes for the states alone leave out the segment
+// that none continues from.
+template <typename TIn, bool kOut>
+__global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const __grid_constant__ Passes<TIn> A, const Shape P) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  pdl_wait();
+  const int nz = kOut ? P.nseg : P.nseg - 1, role = blockIdx.z / nz, z = blockIdx.z - role * nz;
+  if (A.p[role].reverse)
+    scan_segment<TIn, true, kOut>(A.p[role], P, kOut ? z : z + 1, smem_raw);
+  else
+    scan_segment<TIn, false, kOut>(A.p[role], P, z, smem_raw);
+}
+
 // One thread per 4 columns of a state row, along the segments.
-template <typename TIn> __global__ void __launch_bounds__(256) linattn_join_kernel(const Pass<TIn> A, const Shape P) {
+template <typename TIn> __global__ void __launch_bounds__(256) linattn_join_kernel(const __grid_constant__ Passes<TIn> passes,
+                                                                                    const Shape P) {
   const int h = blockIdx.x, b = blockIdx.y;
+  const Pass<TIn> &A = passes.p[blockIdx.z >> 2];
   pdl_wait();
   const SeqBounds sb = seq_bounds(P.cu_seqlens, b, P.T, P.total_T);
   if (sb.len < 0) return;
   const long long segs = (static_cast<long long>(sb.len) + P.seg_len - 1) / P.seg_len;
   const int n = static_cast<int>(segs < 1 ? 1 : segs < P.nseg ? segs : P.nseg);
   const long long pair = static_cast<long long>(b) * P.H + h;
-  const int e4 = blockIdx.z * 256 + threadIdx.x, row = e4 >> 4, col = 4 * (e4 & 15);
+  const int e4 = (blockIdx.z & 3) * 256 + threadIdx.x, row = e4 >> 4, col = 4 * (e4 & 15);
   const double w = P.w[h];
   const float wl = static_cast<float>(powi(w, P.seg_len));
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -175,28 +186,27 @@ template <typename TIn> __global__ void __launch_bounds__(256) linattn_join_kern
 }  // namespace lin
 
 template <typename TIn>
-cudaError_t launch_linattn_scan(const lin::Pass<TIn> &A, const lin::Shape &P, int B, cudaStream_t stream) {
+cudaError_t launch_linattn_scan(const lin::Passes<TIn> &A, const lin::Shape &P, int B, cudaStream_t stream) {
   using namespace lin;
-  auto run = [&](auto kern, int nz) -> cudaError_t {
-    if (nz <= 0) return cudaSuccess;
-    kern<<<dim3(P.H, B, nz), kThreads, Tile<TIn>::kSmem, stream>>>(A, P);
-    return cudaGetLastError();
-  };
-  if (!A.state_only)
-    return A.reverse ? run(linattn_scan_kernel<TIn, true, true>, P.nseg) : run(linattn_scan_kernel<TIn, false, true>, P.nseg);
-  return A.reverse ? run(linattn_scan_kernel<TIn, true, false>, P.nseg - 1)
-                   : run(linattn_scan_kernel<TIn, false, false>, P.nseg - 1);
-}
-
-template <typename TIn>
-cudaError_t launch_linattn_join(const lin::Pass<TIn> &A, const lin::Shape &P, int B, cudaStream_t stream) {
-  lin::linattn_join_kernel<TIn><<<dim3(P.H, B, 4), 256, 0, stream>>>(A, P);
+  const int nz = A.state_only ? P.nseg - 1 : P.nseg;
+  if (nz <= 0) return cudaSuccess;
+  const dim3 grid(P.H, B, nz * A.n);
+  if (A.state_only)
+    linattn_scan_kernel<TIn, false><<<grid, kThreads, Tile<TIn>::kSmem, stream>>>(A, P);
+  else
+    linattn_scan_kernel<TIn, true><<<grid, kThreads, Tile<TIn>::kSmem, stream>>>(A, P);
   return cudaGetLastError();
 }
 
-template cudaError_t launch_linattn_scan<float>(const lin::Pass<float> &, const lin::Shape &, int, cudaStream_t);
-template cudaError_t launch_linattn_scan<uint16_t>(const lin::Pass<uint16_t> &, const lin::Shape &, int, cudaStream_t);
-template cudaError_t launch_linattn_join<float>(const lin::Pass<float> &, const lin::Shape &, int, cudaStream_t);
-template cudaError_t launch_linattn_join<uint16_t>(const lin::Pass<uint16_t> &, const lin::Shape &, int, cudaStream_t);
+template <typename TIn>
+cudaError_t launch_linattn_join(const lin::Passes<TIn> &A, const lin::Shape &P, int B, cudaStream_t stream) {
+  lin::linattn_join_kernel<TIn><<<dim3(P.H, B, 4 * A.n), 256, 0, stream>>>(A, P);
+  return cudaGetLastError();
+}
+
+template cudaError_t launch_linattn_scan<float>(const lin::Passes<float> &, const lin::Shape &, int, cudaStream_t);
+template cudaError_t launch_linattn_scan<uint16_t>(const lin::Passes<uint16_t> &, const lin::Shape &, int, cudaStream_t);
+template cudaError_t launch_linattn_join<float>(const lin::Passes<float> &, const lin::Shape &, int, cudaStream_t);
+template cudaError_t launch_linattn_join<uint16_t>(const lin::Passes<uint16_t> &, const lin::Shape &, int, cudaStream_t);
 
 }  // namespace rwkv7

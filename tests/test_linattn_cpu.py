@@ -131,7 +131,8 @@ def test_workspace_sizes():
     assert lib7.rwkv7_linattn_workspace(64, 4096, 64) == 0  # enough chains as they are
     n = lib7.rwkv7_linattn_workspace(1, 4096, 12)
     assert n > 0 and n % (12 * 64 * 64 * 4) == 0
-    assert lib7.rwkv7_linattn_backward_workspace(1, 4096, 12) == 3 * n
+    n = lib7.rwkv7_linattn_backward_workspace(1, 4096, 12)
+    assert n > 0 and n % (3 * 12 * 64 * 64 * 4) == 0
     assert lib7.rwkv7_layer_norm_workspace(True, 0, 1, 64) == 0
     assert lib7.rwkv7_layer_norm_workspace(True, 5, 0, 64) == 0
 
