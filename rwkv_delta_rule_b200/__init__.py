@@ -410,26 +410,39 @@ def rwkv7_wkv_backward_bf16(r, w, k, v, a, b, states, dy, ds_out, dr, dw, dk, dv
 
 # ---- linear attention with one decay per head, and the layer norm --------------------------------------
 
-class _Where:
-    """The device and stream of a call: its tensors lie on one device, which need not be the current one."""
+def _fits(t, name: str, dtype, shape, device) -> int:
+    """The address of ``t``, which has to be a contiguous tensor of this type and shape on ``device``."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _check(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}: one device is wanted")
+    return t.data_ptr()
 
-    def __init__(self, stream, first, *rest):
-        for t in (first,) + rest:
-            if t is not None and t.device != first.device:
-                raise ValueError(f"tensors on {first.device} and {t.device}: one device is wanted")
-        self.device = first.device
-        if stream is None:
-            stream = torch.cuda.current_stream(first.device)
-        elif isinstance(stream, torch.cuda.Stream) and stream.device != first.device:
-            raise ValueError(f"a stream of {stream.device} for tensors on {first.device}")
-        self.stream = _stream(stream)
 
-    def call(self, name, *args):
-        if torch.cuda.current_device() == self.device.index:
-            _call(name, *args, self.stream)
-        else:
-            with torch.cuda.device(self.device):
-                _call(name, *args, self.stream)
+def _fits_or_none(t, name: str, dtype, shape, device) -> Optional[int]:
+    return None if t is None else _fits(t, name, dtype, shape, device)
+
+
+def _device_of(t, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _call_on(device, stream, name: str, *args) -> None:
+    """The entry point on a stream of the tensors' device, which need not be the current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device != device:
+            raise ValueError(f"a stream of {stream.device} for tensors on {device}")
+        stream = stream.cuda_stream
+    else:
+        stream = int(stream)
+    if torch.cuda.current_device() == device.index:
+        _call(name, *args, stream)
+    else:
+        with torch.cuda.device(device):
+            _call(name, *args, stream)
 
 
 def _on(stream, device):
@@ -446,12 +459,13 @@ def _workspace(n: int, device) -> Optional[torch.Tensor]:
     return torch.empty(n, dtype=torch.uint8, device=device) if n > 0 else None
 
 
-def _check_workspace(ws) -> int:
+def _workspace_args(ws, device):
+    """(address, bytes) of a workspace, or of none."""
     if ws is None:
-        return 0
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    return ws.numel() * ws.element_size()
+        return None, 0
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def rwkv7_linattn_workspace(B: int, max_T: int, H: int) -> int:
@@ -464,19 +478,20 @@ def rwkv7_linattn_backward_workspace(B: int, T: int, H: int) -> int:
     return int(load_library().rwkv7_linattn_backward_workspace(int(B), int(T), int(H)))
 
 
+def _dims(t, name: str, layout: str):
+    if t.dim() != layout.count(",") + 1:
+        raise ValueError(f"{name} must be [{layout}], got {tuple(t.shape)}")
+    return t.shape
+
+
 def _linattn_prefill(name, dtype, r, k, v, w, s_in, y, s_out, workspace, stream):
-    _check(r, "r", dtype)
-    if r.dim() != 4:
-        raise ValueError(f"r must be [B, T, H, 64], got {tuple(r.shape)}")
-    B, T, H, N = r.shape
-    for nm, t in (("k", k), ("v", v), ("y", y)):
-        _check(t, nm, dtype, (B, T, H, N))
-    _check(w, "w", torch.float32, (H,))
-    _check(s_in, "s_in", torch.float32, (B, H, N, N), allow_none=True)
-    _check(s_out, "s_out", torch.float32, (B, H, N, N))
-    nb = _check_workspace(workspace)
-    _Where(stream, r, k, v, w, s_in, y, s_out, workspace).call(
-        name, B, T, H, N, *[_ptr(t) for t in (r, k, v, w, s_in, y, s_out, workspace)], nb)
+    dev = _device_of(r, "r")
+    B, T, H, N = shape = _dims(r, "r", "B, T, H, 64")
+    states = (B, H, N, N)
+    _call_on(dev, stream, name, B, T, H, N, _fits(r, "r", dtype, shape, dev), _fits(k, "k", dtype, shape, dev),
+             _fits(v, "v", dtype, shape, dev), _fits(w, "w", torch.float32, (H,), dev),
+             _fits_or_none(s_in, "s_in", torch.float32, states, dev), _fits(y, "y", dtype, shape, dev),
+             _fits(s_out, "s_out", torch.float32, states, dev), *_workspace_args(workspace, dev))
 
 
 def rwkv7_linattn_prefill(r, k, v, w, s_in, y, s_out, workspace=None, stream=None) -> None:
@@ -493,33 +508,23 @@ def rwkv7_linattn_prefill_bf16(r, k, v, w, s_in, y, s_out, workspace=None, strea
 def rwkv7_linattn_prefill_varlen_bf16(cu_seqlens, max_T, r, k, v, w, s_in, y, s_out, workspace=None,
                                       stream=None) -> None:
     """Ragged bfloat16 prefill: operands / y ``[total_T,H,64]`` packed, ``cu_seqlens`` int32 ``[B+1]`` on the device."""
-    _check(r, "r", torch.bfloat16)
-    if r.dim() != 3:
-        raise ValueError(f"r must be [total_T, H, 64], got {tuple(r.shape)}")
-    total, H, N = r.shape
+    dev, bf16 = _device_of(r, "r"), torch.bfloat16
+    total, H, N = shape = _dims(r, "r", "total_T, H, 64")
     Bn = cu_seqlens.numel() - 1
-    _check(cu_seqlens, "cu_seqlens", torch.int32, (Bn + 1,))
-    for nm, t in (("k", k), ("v", v), ("y", y)):
-        _check(t, nm, torch.bfloat16, (total, H, N))
-    _check(w, "w", torch.float32, (H,))
-    _check(s_in, "s_in", torch.float32, (Bn, H, N, N), allow_none=True)
-    _check(s_out, "s_out", torch.float32, (Bn, H, N, N))
-    nb = _check_workspace(workspace)
-    _Where(stream, r, k, v, w, s_in, y, s_out, cu_seqlens, workspace).call(
-        "rwkv7_linattn_prefill_varlen_bf16", Bn, total, int(max_T), H, N,
-        *[_ptr(t) for t in (cu_seqlens, r, k, v, w, s_in, y, s_out, workspace)], nb)
+    states = (Bn, H, N, N)
+    _call_on(dev, stream, "rwkv7_linattn_prefill_varlen_bf16", Bn, total, int(max_T), H, N,
+             _fits(cu_seqlens, "cu_seqlens", torch.int32, (Bn + 1,), dev), _fits(r, "r", bf16, shape, dev),
+             _fits(k, "k", bf16, shape, dev), _fits(v, "v", bf16, shape, dev), _fits(w, "w", torch.float32, (H,), dev),
+             _fits_or_none(s_in, "s_in", torch.float32, states, dev), _fits(y, "y", bf16, shape, dev),
+             _fits(s_out, "s_out", torch.float32, states, dev), *_workspace_args(workspace, dev))
 
 
 def _linattn_decode(name, dtype, r, k, v, w, s_inout, y, stream):
-    _check(r, "r", dtype)
-    if r.dim() != 3:
-        raise ValueError(f"r must be [B, H, 64], got {tuple(r.shape)}")
-    B, H, N = r.shape
-    for nm, t in (("k", k), ("v", v), ("y", y)):
-        _check(t, nm, dtype, (B, H, N))
-    _check(w, "w", torch.float32, (H,))
-    _check(s_inout, "s_inout", torch.float32, (B, H, N, N))
-    _Where(stream, r, k, v, w, s_inout, y).call(name, B, H, N, *[_ptr(t) for t in (r, k, v, w, s_inout, y)])
+    dev = _device_of(r, "r")
+    B, H, N = shape = _dims(r, "r", "B, H, 64")
+    _call_on(dev, stream, name, B, H, N, _fits(r, "r", dtype, shape, dev), _fits(k, "k", dtype, shape, dev),
+             _fits(v, "v", dtype, shape, dev), _fits(w, "w", torch.float32, (H,), dev),
+             _fits(s_inout, "s_inout", torch.float32, (B, H, N, N), dev), _fits(y, "y", dtype, shape, dev))
 
 
 def rwkv7_linattn_decode(r, k, v, w, s_inout, y, stream=None) -> None:
@@ -535,18 +540,15 @@ def rwkv7_linattn_decode_bf16(r, k, v, w, s_inout, y, stream=None) -> None:
 def rwkv7_linattn_backward_bf16(r, k, v, w, s_in, dy, ds_out, dr, dk, dv, ds_in, workspace=None, stream=None) -> None:
     """Gradients of a loss with dL/dy = ``dy`` (bf16) and dL/ds_out = ``ds_out`` (float32 or None) with respect
     to r, k, v (bf16 ``[B,T,H,64]``) and s_in (``ds_in`` float32 or None)."""
-    _check(r, "r", torch.bfloat16)
-    if r.dim() != 4:
-        raise ValueError(f"r must be [B, T, H, 64], got {tuple(r.shape)}")
-    B, T, H, N = r.shape
-    for nm, t in (("k", k), ("v", v), ("dy", dy), ("dr", dr), ("dk", dk), ("dv", dv)):
-        _check(t, nm, torch.bfloat16, (B, T, H, N))
-    _check(w, "w", torch.float32, (H,))
-    for nm, t in (("s_in", s_in), ("ds_out", ds_out), ("ds_in", ds_in)):
-        _check(t, nm, torch.float32, (B, H, N, N), allow_none=True)
-    nb = _check_workspace(workspace)
-    ts = (r, k, v, w, s_in, dy, ds_out, dr, dk, dv, ds_in, workspace)
-    _Where(stream, *ts).call("rwkv7_linattn_backward_bf16", B, T, H, N, *[_ptr(t) for t in ts], nb)
+    dev, bf16 = _device_of(r, "r"), torch.bfloat16
+    B, T, H, N = shape = _dims(r, "r", "B, T, H, 64")
+    states = (B, H, N, N)
+    _call_on(dev, stream, "rwkv7_linattn_backward_bf16", B, T, H, N, _fits(r, "r", bf16, shape, dev),
+             _fits(k, "k", bf16, shape, dev), _fits(v, "v", bf16, shape, dev), _fits(w, "w", torch.float32, (H,), dev),
+             _fits_or_none(s_in, "s_in", torch.float32, states, dev), _fits(dy, "dy", bf16, shape, dev),
+             _fits_or_none(ds_out, "ds_out", torch.float32, states, dev), _fits(dr, "dr", bf16, shape, dev),
+             _fits(dk, "dk", bf16, shape, dev), _fits(dv, "dv", bf16, shape, dev),
+             _fits_or_none(ds_in, "ds_in", torch.float32, states, dev), *_workspace_args(workspace, dev))
 
 
 def rwkv7_layer_norm_workspace(bf16: bool, M: int, G: int, D: int) -> int:
@@ -554,22 +556,13 @@ def rwkv7_layer_norm_workspace(bf16: bool, M: int, G: int, D: int) -> int:
     return int(load_library().rwkv7_layer_norm_workspace(int(bool(bf16)), int(M), int(G), int(D)))
 
 
-def _norm_shape(x, name):
-    if x.dim() != 3:
-        raise ValueError(f"{name} must be [M, G, D], got {tuple(x.shape)}")
-    return x.shape
-
-
 def _layer_norm(name, dtype, x, weight, bias, eps, y, mean, rstd, stream):
-    _check(x, "x", dtype)
-    M, G, D = _norm_shape(x, "x")
-    _check(y, "y", dtype, (M, G, D))
-    for nm, t in (("weight", weight), ("bias", bias)):
-        _check(t, nm, torch.float32, (G, D), allow_none=True)
-    for nm, t in (("mean", mean), ("rstd", rstd)):
-        _check(t, nm, torch.float32, (M, G), allow_none=True)
-    _Where(stream, x, weight, bias, y, mean, rstd).call(name, M, G, D, float(eps),
-                                                        *[_ptr(t) for t in (x, weight, bias, y, mean, rstd)])
+    dev, f32 = _device_of(x, "x"), torch.float32
+    M, G, D = shape = _dims(x, "x", "M, G, D")
+    _call_on(dev, stream, name, M, G, D, float(eps), _fits(x, "x", dtype, shape, dev),
+             _fits_or_none(weight, "weight", f32, (G, D), dev), _fits_or_none(bias, "bias", f32, (G, D), dev),
+             _fits(y, "y", dtype, shape, dev), _fits_or_none(mean, "mean", f32, (M, G), dev),
+             _fits_or_none(rstd, "rstd", f32, (M, G), dev))
 
 
 def rwkv7_layer_norm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None) -> None:
@@ -584,17 +577,13 @@ def rwkv7_layer_norm_bf16(x, weight, bias, eps, y, mean=None, rstd=None, stream=
 
 
 def _layer_norm_backward(name, dtype, dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, stream):
-    _check(x, "x", dtype)
-    M, G, D = _norm_shape(x, "x")
-    for nm, t in (("dy", dy), ("dx", dx)):
-        _check(t, nm, dtype, (M, G, D))
-    for nm, t in (("weight", weight), ("dweight", dweight), ("dbias", dbias)):
-        _check(t, nm, torch.float32, (G, D), allow_none=True)
-    for nm, t in (("mean", mean), ("rstd", rstd)):
-        _check(t, nm, torch.float32, (M, G))
-    nb = _check_workspace(workspace)
-    ts = (dy, x, weight, mean, rstd, dx, dweight, dbias, workspace)
-    _Where(stream, *ts).call(name, M, G, D, *[_ptr(t) for t in ts], nb)
+    dev, f32 = _device_of(x, "x"), torch.float32
+    M, G, D = shape = _dims(x, "x", "M, G, D")
+    _call_on(dev, stream, name, M, G, D, _fits(dy, "dy", dtype, shape, dev), _fits(x, "x", dtype, shape, dev),
+             _fits_or_none(weight, "weight", f32, (G, D), dev), _fits(mean, "mean", f32, (M, G), dev),
+             _fits(rstd, "rstd", f32, (M, G), dev), _fits(dx, "dx", dtype, shape, dev),
+             _fits_or_none(dweight, "dweight", f32, (G, D), dev), _fits_or_none(dbias, "dbias", f32, (G, D), dev),
+             *_workspace_args(workspace, dev))
 
 
 def rwkv7_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, workspace=None,
@@ -761,48 +750,51 @@ def linattn_backward(r, k, v, w, dy, s_in=None, ds_out=None, *, stream=None):
     return dr, dk, dv, ds_in
 
 
-def _norm_view(x, weight, bias, group):
-    """x as [M, G, D]: the channels normalised together are the last dimension, and weight and bias, of
-    shape [D] or [G, D], say whether the dimension before it numbers groups (``group`` where both are None)."""
-    p = weight if weight is not None else bias
-    grouped = p.dim() == 2 if p is not None else group
-    if x.dim() < (2 if grouped else 1):
-        raise ValueError(f"x must have a last dimension of channels, got {tuple(x.shape)}")
-    G, D = (x.shape[-2] if grouped else 1), x.shape[-1]
-    M = x.numel() // (G * D) if G * D else 0
-    return (M, G, D), x.shape[:-1], tuple(x.shape[-2:] if grouped else x.shape[-1:])
+def _norm_shape(x, weight, grouped):
+    """(M, G, D) of x, whose last dimension is normalised; a weight of shape [G, D] or [D] says whether the
+    dimension before it numbers groups (``grouped`` where there is none)."""
+    if weight is not None:
+        grouped = weight.dim() == 2
+    shape = x.shape
+    if len(shape) < (2 if grouped else 1):
+        raise ValueError(f"x must be {'[..., G, D]' if grouped else '[..., D]'}, got {tuple(shape)}")
+    D, G = shape[-1], (shape[-2] if grouped else 1)
+    return x.numel() // max(1, G * D), G, D, tuple(shape[-2:] if grouped else shape[-1:])
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, *, grouped=False, stream=None):
     """Layer norm over the last dimension; returns ``(y, mean, rstd)`` (mean, rstd float32, of x's shape without
     its last dimension).  weight, bias: float32 ``[D]``, or ``[G, D]`` for x ``[..., G, D]`` with a scale for
     each group; ``grouped`` says which where both are None."""
-    (M, G, D), lead, p = _norm_view(x, weight, bias, grouped)
-    for nm, t in (("weight", weight), ("bias", bias)):
-        _check(t, nm, torch.float32, p, allow_none=True)
-    _check(x, "x", x.dtype)
-    with _on(stream, x.device):
+    dev, f32, dtype, shape = _device_of(x, "x"), torch.float32, x.dtype, x.shape
+    M, G, D, p = _norm_shape(x, weight if weight is not None else bias, grouped)
+    f32_x = dtype is f32
+    args = (_fits(x, "x", f32 if f32_x else torch.bfloat16, shape, dev), _fits_or_none(weight, "weight", f32, p, dev),
+            _fits_or_none(bias, "bias", f32, p, dev))
+    with _on(stream, dev):
         y = torch.empty_like(x)
-        mean, rstd = (torch.empty(lead, dtype=torch.float32, device=x.device) for _ in range(2))
-    f = rwkv7_layer_norm if x.dtype == torch.float32 else rwkv7_layer_norm_bf16
-    f(x.view(M, G, D), None if weight is None else weight.view(G, D), None if bias is None else bias.view(G, D), eps,
-      y.view(M, G, D), mean.view(M, G), rstd.view(M, G), stream)
+        mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+        rstd = torch.empty_like(mean)
+    _call_on(dev, stream, "rwkv7_layer_norm" if f32_x else "rwkv7_layer_norm_bf16", M, G, D, float(eps), *args,
+             y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
     return y, mean, rstd
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, *, grouped=False, stream=None):
     """Gradients of ``layer_norm``; returns ``(dx, dweight, dbias)`` (dweight, dbias float32 of weight's shape)."""
-    (M, G, D), lead, p = _norm_view(x, weight, None, grouped)
-    _check(weight, "weight", torch.float32, p, allow_none=True)
-    _check(x, "x", x.dtype)
-    _check(dy, "dy", x.dtype, x.shape)
-    for nm, t in (("mean", mean), ("rstd", rstd)):
-        _check(t, nm, torch.float32, lead)
-    with _on(stream, x.device):
+    dev, f32, shape = _device_of(x, "x"), torch.float32, x.shape
+    M, G, D, p = _norm_shape(x, weight, grouped)
+    f32_x = x.dtype is f32
+    dtype = f32 if f32_x else torch.bfloat16
+    args = (_fits(dy, "dy", dtype, shape, dev), _fits(x, "x", dtype, shape, dev),
+            _fits_or_none(weight, "weight", f32, p, dev), _fits(mean, "mean", f32, shape[:-1], dev),
+            _fits(rstd, "rstd", f32, shape[:-1], dev))
+    n = load_library().rwkv7_layer_norm_workspace(0 if f32_x else 1, M, G, D)
+    with _on(stream, dev):
         dx = torch.empty_like(x)
-        dweight, dbias = (torch.empty(p, dtype=torch.float32, device=x.device) for _ in range(2))
-        ws = _workspace(rwkv7_layer_norm_workspace(x.dtype == torch.bfloat16, M, G, D), x.device)
-    f = rwkv7_layer_norm_backward if x.dtype == torch.float32 else rwkv7_layer_norm_backward_bf16
-    f(dy.view(M, G, D), x.view(M, G, D), None if weight is None else weight.view(G, D), mean.view(M, G),
-      rstd.view(M, G), dx.view(M, G, D), dweight.view(G, D), dbias.view(G, D), ws, stream)
+        dweight = torch.empty(p, dtype=f32, device=dev)
+        dbias = torch.empty_like(dweight)
+        ws = _workspace(n, dev)
+    _call_on(dev, stream, "rwkv7_layer_norm_backward" if f32_x else "rwkv7_layer_norm_backward_bf16", M, G, D, *args,
+             dx.data_ptr(), dweight.data_ptr(), dbias.data_ptr(), None if ws is None else ws.data_ptr(), n)
     return dx, dweight, dbias

@@ -10,74 +10,85 @@
 // Everything is bound by HBM: two tensors forward, three backward, so each element is loaded once, in
 // 16-byte pieces where the rows allow it, and kept in registers between the sums and the result (the
 // variance is that of the centred values, which costs no second load).  A "unit" is a set of lanes
-// that owns one (m, g) vector: 1 to 32 lanes of a warp while it fits there (4 pieces a lane), else a
+// that owns one (m, g) vector: 1 to 32 lanes of a warp while it fits there (2 pieces a lane), else a
 // whole CTA.  A unit keeps its group g and steps over the rows m, so it also keeps its columns' sums
 // for dw and db in registers; CTAs then leave one partial sum each, and a second launch adds those up
 // in a fixed order.  Vectors too long for a CTA's registers are walked in loops instead.
 #include "layer_norm.h"
 
 #include "common.cuh"
+#include "packed.cuh"
 
 namespace rwkv7 {
 namespace ln {
 
 constexpr int kSMs = 148;
 
-// V consecutive elements of T as they lie in memory, and as floats
+// Loads of what is read once: past L1, which keeps the weights.
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+  uint4 u;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "l"(p));
+  return u;
+}
+
+// V consecutive elements of T as they lie in memory.  get / put: element e of the piece is half (o + e) % 2
+// of pair (o + e) / 2, o being where the piece begins in a lane's elements (its multiple of V).
 template <typename T, int V> struct Piece;
 template <> struct Piece<float, 4> {
-  float4 u;
-  __device__ __forceinline__ void load(const float *p) { u = *reinterpret_cast<const float4 *>(p); }
-  __device__ __forceinline__ void zero() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&o)[4]) const { o[0] = u.x; o[1] = u.y; o[2] = u.z; o[3] = u.w; }
-  static __device__ __forceinline__ void store(float *p, const float (&o)[4]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(o[0], o[1], o[2], o[3]);
+  uint4 u;
+  __device__ __forceinline__ void load(const float *p) { u = ld_once(p); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(f32x2 *x, int o) const {
+    x[o / 2] = make2(__uint_as_float(u.x), __uint_as_float(u.y));
+    x[o / 2 + 1] = make2(__uint_as_float(u.z), __uint_as_float(u.w));
+  }
+  static __device__ __forceinline__ void put(float *p, const f32x2 *x, int o) {
+    float4 f;
+    split2(x[o / 2], f.x, f.y);
+    split2(x[o / 2 + 1], f.z, f.w);
+    *reinterpret_cast<float4 *>(p) = f;
   }
 };
-template <> struct Piece<float, 1> {
-  float u;
-  __device__ __forceinline__ void load(const float *p) { u = *p; }
-  __device__ __forceinline__ void zero() { u = 0.f; }
-  __device__ __forceinline__ void get(float (&o)[1]) const { o[0] = u; }
-  static __device__ __forceinline__ void store(float *p, const float (&o)[1]) { *p = o[0]; }
-};
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  return static_cast<uint32_t>(float_to_bf16_bits(lo)) | (static_cast<uint32_t>(float_to_bf16_bits(hi)) << 16);
-}
 template <> struct Piece<uint16_t, 8> {
   uint4 u;
-  __device__ __forceinline__ void load(const uint16_t *p) { u = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void load(const uint16_t *p) { u = ld_once(p); }
   __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ void get(float (&o)[8]) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = __uint_as_float(w[i] << 16);
-      o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  __device__ __forceinline__ void get(f32x2 *x, int o) const {
+    x[o / 2] = unpack2(u.x);
+    x[o / 2 + 1] = unpack2(u.y);
+    x[o / 2 + 2] = unpack2(u.z);
+    x[o / 2 + 3] = unpack2(u.w);
   }
-  static __device__ __forceinline__ void store(uint16_t *p, const float (&o)[8]) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+  static __device__ __forceinline__ void put(uint16_t *p, const f32x2 *x, int o) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(x[o / 2]), pack2(x[o / 2 + 1]), pack2(x[o / 2 + 2]), pack2(x[o / 2 + 3]));
   }
 };
 template <> struct Piece<uint16_t, 2> {
   uint32_t u;
   __device__ __forceinline__ void load(const uint16_t *p) { u = *reinterpret_cast<const uint32_t *>(p); }
   __device__ __forceinline__ void zero() { u = 0u; }
-  __device__ __forceinline__ void get(float (&o)[2]) const {
-    o[0] = __uint_as_float(u << 16);
-    o[1] = __uint_as_float(u & 0xffff0000u);
-  }
-  static __device__ __forceinline__ void store(uint16_t *p, const float (&o)[2]) {
-    *reinterpret_cast<uint32_t *>(p) = pack2(o[0], o[1]);
+  __device__ __forceinline__ void get(f32x2 *x, int o) const { x[o / 2] = unpack2(u); }
+  static __device__ __forceinline__ void put(uint16_t *p, const f32x2 *x, int o) {
+    *reinterpret_cast<uint32_t *>(p) = pack2(x[o / 2]);
   }
 };
-template <> struct Piece<uint16_t, 1> {
-  uint16_t u;
-  __device__ __forceinline__ void load(const uint16_t *p) { u = *p; }
+template <typename T> struct Piece<T, 1> {
+  T u;
+  __device__ __forceinline__ void load(const T *p) { u = *p; }
   __device__ __forceinline__ void zero() { u = 0; }
-  __device__ __forceinline__ void get(float (&o)[1]) const { o[0] = bf16_bits_to_float(u); }
-  static __device__ __forceinline__ void store(uint16_t *p, const float (&o)[1]) { *p = float_to_bf16_bits(o[0]); }
+  __device__ __forceinline__ void get(f32x2 *x, int o) const {
+    float a, b;
+    split2(x[o / 2], a, b);
+    const float f = Elem<T>::load(&u);
+    x[o / 2] = o % 2 ? make2(a, f) : make2(f, 0.f);
+  }
+  static __device__ __forceinline__ void put(T *p, const f32x2 *x, int o) {
+    float a, b;
+    split2(x[o / 2], a, b);
+    Elem<T>::store(p, o % 2 ? b : a);
+  }
 };
 
 template <typename T> struct Args {
@@ -92,46 +103,61 @@ template <typename T> struct Args {
   int lanes, gper, slots, gblocks;
 };
 
-// V float32 parameters from w + c (ones or zeros where there is none); w is only 4-byte aligned for odd D
-template <int V> __device__ __forceinline__ void params(const float *w, long long c, float missing, float (&o)[V]) {
-  if (w == nullptr) {
+// V float32 parameters from w + c, placed as a piece's elements (ones or zeros where there is no w, which
+// is only 4-byte aligned for odd D)
+template <int V> __device__ __forceinline__ void params(const float *w, long long c, float missing, f32x2 *x, int o) {
+  if constexpr (V == 1) {
+    float a, b;
+    split2(x[o / 2], a, b);
+    const float f = w == nullptr ? missing : w[c];
+    x[o / 2] = o % 2 ? make2(a, f) : make2(f, 0.f);
+  } else if (w == nullptr) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = missing;
+    for (int e = 0; e < V; e += 2) x[(o + e) / 2] = make2(missing, missing);
   } else if constexpr (V % 4 == 0) {
 #pragma unroll
     for (int e = 0; e < V; e += 4) {
       const float4 u = *reinterpret_cast<const float4 *>(w + c + e);
-      o[e] = u.x; o[e + 1] = u.y; o[e + 2] = u.z; o[e + 3] = u.w;
+      x[(o + e) / 2] = make2(u.x, u.y);
+      x[(o + e) / 2 + 1] = make2(u.z, u.w);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = w[c + e];
+    for (int e = 0; e < V; e += 2) {
+      const float2 u = *reinterpret_cast<const float2 *>(w + c + e);
+      x[(o + e) / 2] = make2(u.x, u.y);
+    }
   }
 }
 
-// Sums over a unit's lanes.  Block units: the warps' sums meet in red (2 x 32 floats per call site
-// parity), with one barrier per call; a call's slots are rewritten two calls later at the earliest.
-template <bool kBlock> __device__ __forceinline__ float2 unit_sum(float2 v, int lanes, float2 *red, int &turn) {
-  const int top = kBlock ? 16 : lanes >> 1;
-  for (int off = top; off >= 1; off >>= 1) {
+__device__ __forceinline__ float lane_sum(float v, int lanes) {
+  for (int off = lanes >> 1; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+__device__ __forceinline__ float2 lane_sum(float2 v, int lanes) {
+  for (int off = lanes >> 1; off >= 1; off >>= 1) {
     v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
     v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
   }
-  if (kBlock) {
-    float2 *slot = red + 32 * turn;
-    turn ^= 1;
-    const int warps = blockDim.x >> 5;
-    if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float2 t = (threadIdx.x & 31) < warps ? slot[threadIdx.x & 31] : make_float2(0.f, 0.f);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) {
-      t.x += __shfl_xor_sync(0xffffffffu, t.x, off);
-      t.y += __shfl_xor_sync(0xffffffffu, t.y, off);
-    }
-    v = t;
-  }
   return v;
+}
+// Sums over a unit's lanes.  Block units: the warps' sums meet in red (two sets of 32), with one barrier per
+// call; a set is rewritten two calls later at the earliest.  `warps`: of the CTA, rounded up to a power of 2.
+template <bool kBlock, typename F> __device__ __forceinline__ F unit_sum(F v, int lanes, int warps, F *red, int &turn) {
+  if (!kBlock) return lane_sum(v, lanes);
+  v = lane_sum(v, 32);
+  F *slot = red + 32 * turn;
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int l = threadIdx.x & (warps - 1);
+  F t{};
+  if (l < static_cast<int>(blockDim.x >> 5)) t = slot[l];
+  return lane_sum(t, warps);
+}
+__device__ __forceinline__ int warps_pow2() {
+  const int w = blockDim.x >> 5;
+  return w <= 1 ? 1 : 1 << (32 - __clz(w - 1));
 }
 
 // Where a thread stands: its unit's group, the row it begins with, the step between its rows.
@@ -153,61 +179,109 @@ template <bool kBlock, typename T> __device__ __forceinline__ Place place(const 
   return p;
 }
 
+// The vector of row m of a place, zeros where there is none.
+template <typename T, int V, int NV>
+__device__ __forceinline__ void fetch(const Args<T> &A, const T *from, const Place &p, long long m, Piece<T, V> (&u)[NV]) {
+  const T *row = from + (m * A.G + p.g) * A.D;
+  const bool on = p.active && m < A.M;
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int c = (n * A.lanes + p.lane) * V;
+    if (on && c < A.D) u[n].load(row + c); else u[n].zero();
+  }
+}
+
+// Registers a thread may take with E elements.  Forward: two float32 parameters (beyond 16 elements they
+// are read again from L1) and the value per element, and one or two rows fetched ahead: with rows of
+// 8 KB, 48 KB are in flight per SM.  Backward: the weight, two sums, and the row under way and the next of
+// two tensors.
+constexpr int forward_regs(int E) { return E <= 8 ? 64 : E <= 16 ? 80 : 128; }
+constexpr int backward_regs(int E) { return E <= 8 ? 80 : 128; }
+constexpr int kMaxThreads = 512;
+
 template <typename T, int V, int NV, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? 1024 : 256) layer_norm_kernel(const Args<T> A) {
-  __shared__ float2 red[64];
+__global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(forward_regs(V *NV))
+    layer_norm_kernel(const Args<T> A) {
+  constexpr int kPairs = (V * NV + 1) / 2, kAhead = V * NV * sizeof(T) <= 32 ? 2 : 1;
+  constexpr bool kKeepW = V * NV <= 16;
+  __shared__ float red[64];
   int turn = 0;
   pdl_wait();
   pdl_trigger();
   const Place p = place<kBlock>(A);
+  const int warps = warps_pow2();
   const float inv = 1.f / static_cast<float>(A.D);
+  f32x2 w[kPairs] = {}, b[kPairs] = {};
+#pragma unroll
+  for (int n = 0; n < NV; ++n) {
+    const int c = (n * A.lanes + p.lane) * V;
+    if (kKeepW && p.active && c < A.D) {
+      params<V>(A.w, static_cast<long long>(p.g) * A.D + c, 1.f, w, n * V);
+      params<V>(A.b, static_cast<long long>(p.g) * A.D + c, 0.f, b, n * V);
+    }
+  }
   // every lane of a warp takes the same number of turns (the sums are over whole warps)
   const long long rows = (A.M + p.step - 1) / p.step;
+  Piece<T, V> next[kAhead][NV];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) fetch(A, A.x, p, p.m + k * p.step, next[k]);
   for (long long i = 0; i < rows; ++i) {
     const long long m = p.m + i * p.step;
-    const bool on = p.active && m < A.M;
-    const long long base = (m * A.G + p.g) * A.D;
-    Piece<T, V> u[NV];
-    float x[NV][V];
-    float s = 0.f;
+    f32x2 x[kPairs] = {}, s2 = make2(0.f, 0.f);
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      next[0][n].get(x, n * V);
+#pragma unroll
+      for (int k = 0; k + 1 < kAhead; ++k) next[k][n] = next[k + 1][n];
+    }
+    fetch(A, A.x, p, m + kAhead * p.step, next[kAhead - 1]);
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) s2 = add2(s2, x[e]);
+    float s, t;
+    split2(s2, s, t);
+    const float mean = unit_sum<kBlock>(s + t, A.lanes, warps, red, turn) * inv;
+    // centred values; what lies past the vector's end counts as zero
+    const f32x2 mm = make2(-mean, -mean);
+    f32x2 q2 = make2(0.f, 0.f);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int c = (n * A.lanes + p.lane) * V;
-      if (on && c < A.D) u[n].load(A.x + base + c); else u[n].zero();
-    }
+      if constexpr (V == 1) {
+        float a, z;
+        split2(x[n / 2], a, z);
+        const float d = c < A.D ? (n % 2 ? z : a) - mean : 0.f;
+        x[n / 2] = n % 2 ? make2(a, d) : make2(d, z);
+        q2 = fma2(make2(d, 0.f), make2(d, 0.f), q2);
+      } else if (c < A.D) {
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      u[n].get(x[n]);
-#pragma unroll
-      for (int e = 0; e < V; ++e) s += x[n][e];
-    }
-    const float mean = unit_sum<kBlock>(make_float2(s, 0.f), A.lanes, red, turn).x * inv;
-    float q = 0.f;
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int c = (n * A.lanes + p.lane) * V;
-      if (c < A.D) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          x[n][e] -= mean;
-          q = fmaf(x[n][e], x[n][e], q);
+        for (int e = n * V / 2; e < (n + 1) * V / 2; ++e) {
+          x[e] = add2(x[e], mm);
+          q2 = fma2(x[e], x[e], q2);
         }
       }
     }
-    const float var = unit_sum<kBlock>(make_float2(q, 0.f), A.lanes, red, turn).x * inv;
+    split2(q2, s, t);
+    const float var = unit_sum<kBlock>(s + t, A.lanes, warps, red, turn) * inv;
     const float rstd = 1.f / sqrtf(var + A.eps);
-    if (!on) continue;
+    if (!(p.active && m < A.M)) continue;
+    T *out = A.out + (m * A.G + p.g) * A.D;
+    const f32x2 rr = make2(rstd, rstd);
+    if constexpr (kKeepW) {
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) x[e] = fma2(mul2(x[e], rr), w[e], b[e]);
+    }
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int c = (n * A.lanes + p.lane) * V;
       if (c < A.D) {
-        float w[V], b[V];
-        const long long pc = static_cast<long long>(p.g) * A.D + c;
-        params<V>(A.w, pc, 1.f, w);
-        params<V>(A.b, pc, 0.f, b);
+        if constexpr (!kKeepW) {
+          f32x2 wp[V / 2], bp[V / 2];
+          params<V>(A.w, static_cast<long long>(p.g) * A.D + c, 1.f, wp, 0);
+          params<V>(A.b, static_cast<long long>(p.g) * A.D + c, 0.f, bp, 0);
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[n][e] = fmaf(x[n][e] * rstd, w[e], b[e]);
-        Piece<T, V>::store(A.out + base + c, x[n]);
+          for (int e = 0; e < V / 2; ++e) x[n * V / 2 + e] = fma2(mul2(x[n * V / 2 + e], rr), wp[e], bp[e]);
+        }
+        Piece<T, V>::put(out + c, x, n * V);
       }
     }
     if (p.lane == 0) {
@@ -217,76 +291,87 @@ __global__ void __launch_bounds__(kBlock ? 1024 : 256) layer_norm_kernel(const A
   }
 }
 
-// threads of a CTA unit in the backward: 3 float32 values per element are kept
-constexpr int backward_threads(int v, int nv) { return v * nv > 8 ? 512 : 1024; }
-
 template <typename T, int V, int NV, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? backward_threads(V, NV) : 256) layer_norm_backward_kernel(const Args<T> A) {
+__global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(backward_regs(V *NV))
+    layer_norm_backward_kernel(const Args<T> A) {
+  constexpr int kPairs = (V * NV + 1) / 2;
   __shared__ float2 red[64];
   extern __shared__ float sums[];  // units of a warp only: [2][slots][gper * lanes * NV * V]
   int turn = 0;
   pdl_wait();
   pdl_trigger();
   const Place p = place<kBlock>(A);
+  const int warps = warps_pow2();
   const float inv = 1.f / static_cast<float>(A.D);
-  float w[NV][V], aw[NV][V], ab[NV][V];
+  f32x2 w[kPairs] = {}, aw[kPairs] = {}, ab[kPairs] = {};
 #pragma unroll
   for (int n = 0; n < NV; ++n) {
     const int c = (n * A.lanes + p.lane) * V;
-#pragma unroll
-    for (int e = 0; e < V; ++e) w[n][e] = aw[n][e] = ab[n][e] = 0.f;
-    if (p.active && c < A.D) params<V>(A.w, static_cast<long long>(p.g) * A.D + c, 1.f, w[n]);
+    if (p.active && c < A.D) params<V>(A.w, static_cast<long long>(p.g) * A.D + c, 1.f, w, n * V);
   }
   const long long rows = (A.M + p.step - 1) / p.step;
+  Piece<T, V> nx[NV], nd[NV];
+  float nmean = 0.f, nrstd = 0.f;
+  auto fetch_all = [&](long long m) {
+    fetch(A, A.x, p, m, nx);
+    fetch(A, A.dy, p, m, nd);
+    if (p.active && m < A.M) {
+      nmean = A.mean[m * A.G + p.g];
+      nrstd = A.rstd[m * A.G + p.g];
+    }
+  };
+  fetch_all(p.m);
   for (long long i = 0; i < rows; ++i) {
     const long long m = p.m + i * p.step;
-    const bool on = p.active && m < A.M;
-    const long long base = (m * A.G + p.g) * A.D;
     Piece<T, V> ux[NV], ud[NV];
-    const float mean = on ? A.mean[m * A.G + p.g] : 0.f, rstd = on ? A.rstd[m * A.G + p.g] : 0.f;
+    const float rstd = nrstd;
+    const f32x2 rr = make2(rstd, rstd), mm = make2(-nmean, -nmean);
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      ux[n] = nx[n];
+      ud[n] = nd[n];
+    }
+    fetch_all(m + p.step);
+    f32x2 sg = make2(0.f, 0.f), sx = make2(0.f, 0.f);  // sums of g and g xh
+    // (past the vector's end dy is zero, and so is what it adds)
+    {
+      f32x2 x[kPairs] = {}, d[kPairs] = {};
+#pragma unroll
+      for (int n = 0; n < NV; ++n) {
+        ux[n].get(x, n * V);
+        ud[n].get(d, n * V);
+      }
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) {
+        const f32x2 xh = mul2(add2(x[e], mm), rr), g = mul2(d[e], w[e]);
+        sg = add2(sg, g);
+        sx = fma2(g, xh, sx);
+        aw[e] = fma2(d[e], xh, aw[e]);
+        ab[e] = add2(ab[e], d[e]);
+      }
+    }
+    float a, b, c0, d0;
+    split2(sg, a, b);
+    split2(sx, c0, d0);
+    const float2 s = unit_sum<kBlock>(make_float2(a + b, c0 + d0), A.lanes, warps, red, turn);
+    if (!(p.active && m < A.M)) continue;
+    // dx = rstd (g - mg - xh mgx)
+    const float mg = -s.x * inv * rstd, mgx = -s.y * inv * rstd;
+    const f32x2 mg2 = make2(mg, mg), mgx2 = make2(mgx, mgx);
+    T *out = A.out + (m * A.G + p.g) * A.D;
+    f32x2 x[kPairs] = {}, d[kPairs] = {};
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      ux[n].get(x, n * V);
+      ud[n].get(d, n * V);
+    }
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e)
+      d[e] = fma2(mul2(d[e], w[e]), rr, fma2(mul2(add2(x[e], mm), rr), mgx2, mg2));
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
       const int c = (n * A.lanes + p.lane) * V;
-      if (on && c < A.D) {
-        ux[n].load(A.x + base + c);
-        ud[n].load(A.dy + base + c);
-      } else {
-        ux[n].zero();
-        ud[n].zero();
-      }
-    }
-    float2 s = make_float2(0.f, 0.f);  // sums of g and g xh
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      float x[V], d[V];
-      ux[n].get(x);
-      ud[n].get(d);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xh = (x[e] - mean) * rstd, g = d[e] * w[n][e];
-        s.x += g;
-        s.y = fmaf(g, xh, s.y);
-        aw[n][e] = fmaf(d[e], xh, aw[n][e]);
-        ab[n][e] += d[e];
-      }
-    }
-    s = unit_sum<kBlock>(s, A.lanes, red, turn);
-    if (!on) continue;
-    const float mg = s.x * inv, mgx = s.y * inv;
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int c = (n * A.lanes + p.lane) * V;
-      if (c < A.D) {
-        float x[V], d[V];
-        ux[n].get(x);
-        ud[n].get(d);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float xh = (x[e] - mean) * rstd;
-          d[e] = rstd * (fmaf(d[e], w[n][e], -mg) - xh * mgx);
-        }
-        Piece<T, V>::store(A.out + base + c, d);
-      }
+      if (c < A.D) Piece<T, V>::put(out + c, d, n * V);
     }
   }
   if (A.partial == nullptr) return;
@@ -299,10 +384,12 @@ __global__ void __launch_bounds__(kBlock ? backward_threads(V, NV) : 256) layer_
       const int c = (n * A.lanes + p.lane) * V;
       if (p.active && c < A.D) {
         const long long pc = static_cast<long long>(p.g) * A.D + c;
+        Piece<float, V % 4 == 0 ? 4 : 1>::put(out + pc, aw, n * V);
+        Piece<float, V % 4 == 0 ? 4 : 1>::put(out + GD + pc, ab, n * V);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          out[pc + e] = aw[n][e];
-          out[GD + pc + e] = ab[n][e];
+        for (int e = V % 4 == 0 ? 4 : 1; e < V; e += V % 4 == 0 ? 4 : 1) {
+          Piece<float, V % 4 == 0 ? 4 : 1>::put(out + pc + e, aw, n * V + e);
+          Piece<float, V % 4 == 0 ? 4 : 1>::put(out + GD + pc + e, ab, n * V + e);
         }
       }
     }
@@ -315,8 +402,8 @@ __global__ void __launch_bounds__(kBlock ? backward_threads(V, NV) : 256) layer_
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const int col = col0 + (n * A.lanes + p.lane) * V + e;
-        sums[slot * width + col] = aw[n][e];
-        sums[(A.slots + slot) * width + col] = ab[n][e];
+        Piece<float, 1>::put(sums + slot * width + col, aw, n * V + e);
+        Piece<float, 1>::put(sums + (A.slots + slot) * width + col, ab, n * V + e);
       }
   }
   __syncthreads();
@@ -332,7 +419,7 @@ __global__ void __launch_bounds__(kBlock ? backward_threads(V, NV) : 256) layer_
 
 // Vectors that no CTA holds in registers: one CTA per (m, g), read again for each sum.
 template <typename T> __global__ void __launch_bounds__(1024) layer_norm_long_kernel(const Args<T> A) {
-  __shared__ float2 red[64];
+  __shared__ float red[64];
   int turn = 0;
   pdl_wait();
   pdl_trigger();
@@ -340,13 +427,13 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_long_ke
   const long long gc = static_cast<long long>(blockIdx.x - m * A.G) * A.D;
   float s = 0.f;
   for (int c = threadIdx.x; c < A.D; c += blockDim.x) s += Elem<T>::load(A.x + base + c);
-  const float mean = unit_sum<true>(make_float2(s, 0.f), 32, red, turn).x / static_cast<float>(A.D);
+  const float mean = unit_sum<true>(s, 32, 32, red, turn) / static_cast<float>(A.D);
   float q = 0.f;
   for (int c = threadIdx.x; c < A.D; c += blockDim.x) {
     const float d = Elem<T>::load(A.x + base + c) - mean;
     q = fmaf(d, d, q);
   }
-  const float var = unit_sum<true>(make_float2(q, 0.f), 32, red, turn).x / static_cast<float>(A.D);
+  const float var = unit_sum<true>(q, 32, 32, red, turn) / static_cast<float>(A.D);
   const float rstd = 1.f / sqrtf(var + A.eps);
   for (int c = threadIdx.x; c < A.D; c += blockDim.x) {
     const float xh = (Elem<T>::load(A.x + base + c) - mean) * rstd;
@@ -373,7 +460,7 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_backwar
     s.x += g;
     s.y = fmaf(g, xh, s.y);
   }
-  s = unit_sum<true>(s, 32, red, turn);
+  s = unit_sum<true>(s, 32, 32, red, turn);
   const float mg = s.x / static_cast<float>(A.D), mgx = s.y / static_cast<float>(A.D);
   for (int c = threadIdx.x; c < A.D; c += blockDim.x) {
     const float xh = (Elem<T>::load(A.x + base + c) - mean) * rstd;
@@ -408,8 +495,10 @@ __global__ void __launch_bounds__(1024) layer_norm_reduce_kernel(const float *pa
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const long long c = static_cast<long long>(blockIdx.x) * 32 + tx;
   float t = 0.f;
-  if (c < 2 * GD)
+  if (c < 2 * GD) {
+#pragma unroll 8
     for (int i = ty; i < n; i += 32) t += partial[i * 2 * GD + c];
+  }
   part[ty][tx] = t;
   __syncthreads();
   t = part[tx][ty];
@@ -435,7 +524,7 @@ Plan make_plan(size_t elem, int M, int G, int D, bool backward) {
   const int full = static_cast<int>(16 / elem);
   P.v = D % full == 0 ? full : (elem == 2 && D % 2 == 0) ? 2 : 1;
   const int pieces = ceil_div(D, P.v);
-  if (pieces <= 128) {
+  if (pieces <= 64) {
     P.lanes = 1;
     while (P.lanes < pieces && P.lanes < 32) P.lanes *= 2;
     P.nv = ceil_div(pieces, P.lanes);
@@ -446,17 +535,16 @@ Plan make_plan(size_t elem, int M, int G, int D, bool backward) {
   } else {
     P.block = true;
     P.gper = P.slots = 1;
-    // the backward keeps three more values per element, so half as many elements per thread
-    const int most = backward ? 16 / P.v : 32 / P.v;
-    const int cap = most < 8 ? most : 8;
-    for (P.nv = cap >= 2 && pieces >= 256 ? 2 : 1; P.nv < cap && ceil_div(pieces, P.nv) > 512; P.nv *= 2) {}
+    const int most = (backward ? 16 : static_cast<int>(64 / elem)) / P.v, cap = most < 8 ? most : 8;  // pieces per lane
+    for (P.nv = 1; P.nv < cap && ceil_div(pieces, P.nv) > 256; P.nv *= 2) {}
     P.threads = (ceil_div(pieces, P.nv) + 31) / 32 * 32;
     P.lanes = P.threads;
-    if (P.threads > (backward ? backward_threads(P.v, P.nv) : 1024)) P.loop = true;
+    P.loop = P.threads > kMaxThreads;
   }
   P.gblocks = ceil_div(G, P.gper);
   const int rowblocks = ceil_div(M, P.slots);  // CTAs that would take one row per unit
-  const int resident = P.loop ? 2 : backward ? 2048 / P.threads / 2 : 2048 / P.threads;
+  const int regs = backward ? backward_regs(P.v * P.nv) : forward_regs(P.v * P.nv);
+  const int resident = P.loop ? 2 : 65536 / regs / P.threads;
   const int want = ceil_div(static_cast<long long>(kSMs) * (resident > 0 ? resident : 1), P.gblocks);
   P.mblocks = rowblocks < want ? rowblocks : want;
   return P;
@@ -487,10 +575,10 @@ template <typename T, int V, int NV, bool kBlock>
 cudaError_t launch_planned(const Plan &P, const Args<T> &A, bool backward, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(P.gblocks * P.mblocks));
   if (!backward) return launch(layer_norm_kernel<T, V, NV, kBlock>, grid, P.threads, 0, stream, A);
-  if constexpr (kBlock && V * NV > 16) return cudaErrorInvalidValue;  // no plan asks for it
+  if constexpr (V * NV > 16) return cudaErrorInvalidValue;  // no plan asks for it
   size_t smem = 0;
   if (!kBlock && P.slots > 1) smem = sizeof(float) * 2 * P.slots * P.gper * P.lanes * P.nv * P.v;
-  auto kern = layer_norm_backward_kernel<T, V, (kBlock && V * NV > 16 ? 1 : NV), kBlock>;
+  auto kern = layer_norm_backward_kernel<T, V, (V * NV > 16 ? 1 : NV), kBlock>;
   if (smem > 48 * 1024 - 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -503,15 +591,13 @@ template <typename T, int V> cudaError_t launch_v(const Plan &P, const Args<T> &
     switch (P.nv) {
       case 1: return launch_planned<T, V, 1, false>(P, A, backward, stream);
       case 2: return launch_planned<T, V, 2, false>(P, A, backward, stream);
-      case 3: return launch_planned<T, V, 3, false>(P, A, backward, stream);
-      case 4: return launch_planned<T, V, 4, false>(P, A, backward, stream);
     }
   } else {
     switch (P.nv) {
       case 1: return launch_planned<T, V, 1, true>(P, A, backward, stream);
       case 2: return launch_planned<T, V, 2, true>(P, A, backward, stream);
       case 4: return launch_planned<T, V, 4, true>(P, A, backward, stream);
-      case 8: if constexpr (V < 8) return launch_planned<T, V, 8, true>(P, A, backward, stream);
+      case 8: if constexpr (V < 4) return launch_planned<T, V, 8, true>(P, A, backward, stream);
     }
   }
   return cudaErrorInvalidValue;
