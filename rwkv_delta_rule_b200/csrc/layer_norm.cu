@@ -160,11 +160,10 @@ __device__ __forceinline__ int warps_pow2() {
   return w <= 1 ? 1 : 1 << (32 - __clz(w - 1));
 }
 
-// Where a thread stands: its unit's group, the row it begins with, the step between its rows.
+// Where a thread stands: its unit's group g, and `count` rows from m0 on, `step` apart.  Every unit of a CTA goes
+// through `turns` rows (the sums are over whole warps), the last of them perhaps empty.
 struct Place {
-  int lane, unit, g;
-  long long m, step;
-  bool active;
+  int lane, unit, g, m0, step, count, turns;
 };
 template <bool kBlock, typename T> __device__ __forceinline__ Place place(const Args<T> &A) {
   Place p;
@@ -173,22 +172,27 @@ template <bool kBlock, typename T> __device__ __forceinline__ Place place(const 
   const int gb = blockIdx.x % A.gblocks, mb = blockIdx.x / A.gblocks, mblocks = gridDim.x / A.gblocks;
   p.g = gb * A.gper + p.unit % A.gper;
   const int slot = p.unit / A.gper;
-  p.m = static_cast<long long>(mb) * A.slots + slot;
-  p.step = static_cast<long long>(mblocks) * A.slots;
-  p.active = slot < A.slots && p.g < A.G;
+  p.m0 = mb * A.slots + slot;  // below 2^31: mblocks * slots is at most M + slots
+  p.step = mblocks * A.slots;
+  p.turns = (A.M - 1) / p.step + 1;
+  p.count = slot < A.slots && p.g < A.G && p.m0 < A.M ? (A.M - 1 - p.m0) / p.step + 1 : 0;
   return p;
 }
+// The lane's first element in the vector of a unit's first row, and the elements from one of its rows to the next.
+template <typename T> __device__ __forceinline__ long long first_at(const Args<T> &A, const Place &p, int V) {
+  return (static_cast<long long>(p.m0) * A.G + p.g) * A.D + p.lane * V;
+}
+template <typename T> __device__ __forceinline__ long long row_step(const Args<T> &A, const Place &p) {
+  return static_cast<long long>(p.step) * A.G * A.D;
+}
 
-// The vector of row m of a place, zeros where there is none.
+// A lane's pieces of the vector at `row`, zeros past its end (`left` elements are left from the lane's first)
+// and where there is no row.
 template <typename T, int V, int NV>
-__device__ __forceinline__ void fetch(const Args<T> &A, const T *from, const Place &p, long long m, Piece<T, V> (&u)[NV]) {
-  const T *row = from + (m * A.G + p.g) * A.D;
-  const bool on = p.active && m < A.M;
+__device__ __forceinline__ void fetch(const T *row, bool on, int stride, int left, Piece<T, V> (&u)[NV]) {
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int c = (n * A.lanes + p.lane) * V;
-    if (on && c < A.D) u[n].load(row + c); else u[n].zero();
-  }
+  for (int n = 0; n < NV; ++n)
+    if (on && n * stride < left) u[n].load(row + n * stride); else u[n].zero();
 }
 
 // Registers a thread may take with E elements.  Forward: two float32 parameters (beyond 16 elements they
@@ -209,24 +213,23 @@ __global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(forwar
   pdl_wait();
   pdl_trigger();
   const Place p = place<kBlock>(A);
-  const int warps = warps_pow2();
+  const int warps = warps_pow2(), stride = A.lanes * V, left = A.D - p.lane * V;
   const float inv = 1.f / static_cast<float>(A.D);
+  const long long gc = static_cast<long long>(p.g) * A.D + p.lane * V, jump = row_step(A, p);
   f32x2 w[kPairs] = {}, b[kPairs] = {};
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int c = (n * A.lanes + p.lane) * V;
-    if (kKeepW && p.active && c < A.D) {
-      params<V>(A.w, static_cast<long long>(p.g) * A.D + c, 1.f, w, n * V);
-      params<V>(A.b, static_cast<long long>(p.g) * A.D + c, 0.f, b, n * V);
+  for (int n = 0; n < NV; ++n)
+    if (kKeepW && p.count > 0 && n * stride < left) {
+      params<V>(A.w, gc + n * stride, 1.f, w, n * V);
+      params<V>(A.b, gc + n * stride, 0.f, b, n * V);
     }
-  }
-  // every lane of a warp takes the same number of turns (the sums are over whole warps)
-  const long long rows = (A.M + p.step - 1) / p.step;
+  const T *in = A.x + first_at(A, p, V);
+  T *out = A.out + first_at(A, p, V);
+  long long stat = static_cast<long long>(p.m0) * A.G + p.g;
   Piece<T, V> next[kAhead][NV];
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k) fetch(A, A.x, p, p.m + k * p.step, next[k]);
-  for (long long i = 0; i < rows; ++i) {
-    const long long m = p.m + i * p.step;
+  for (int k = 0; k < kAhead; ++k, in += jump) fetch(in, k < p.count, stride, left, next[k]);
+  for (int i = 0; i < p.turns; ++i) {
     f32x2 x[kPairs] = {}, s2 = make2(0.f, 0.f);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
@@ -234,7 +237,8 @@ __global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(forwar
 #pragma unroll
       for (int k = 0; k + 1 < kAhead; ++k) next[k][n] = next[k + 1][n];
     }
-    fetch(A, A.x, p, m + kAhead * p.step, next[kAhead - 1]);
+    fetch(in, p.count - i > kAhead, stride, left, next[kAhead - 1]);
+    in += jump;
 #pragma unroll
     for (int e = 0; e < kPairs; ++e) s2 = add2(s2, x[e]);
     float s, t;
@@ -245,14 +249,13 @@ __global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(forwar
     f32x2 q2 = make2(0.f, 0.f);
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-      const int c = (n * A.lanes + p.lane) * V;
       if constexpr (V == 1) {
         float a, z;
         split2(x[n / 2], a, z);
-        const float d = c < A.D ? (n % 2 ? z : a) - mean : 0.f;
+        const float d = n * stride < left ? (n % 2 ? z : a) - mean : 0.f;
         x[n / 2] = n % 2 ? make2(a, d) : make2(d, z);
         q2 = fma2(make2(d, 0.f), make2(d, 0.f), q2);
-      } else if (c < A.D) {
+      } else if (n * stride < left) {
 #pragma unroll
         for (int e = n * V / 2; e < (n + 1) * V / 2; ++e) {
           x[e] = add2(x[e], mm);
@@ -262,32 +265,32 @@ __global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(forwar
     }
     split2(q2, s, t);
     const float var = unit_sum<kBlock>(s + t, A.lanes, warps, red, turn) * inv;
-    const float rstd = 1.f / sqrtf(var + A.eps);
-    if (!(p.active && m < A.M)) continue;
-    T *out = A.out + (m * A.G + p.g) * A.D;
-    const f32x2 rr = make2(rstd, rstd);
-    if constexpr (kKeepW) {
+    const float rstd = rsqrtf(var + A.eps);  // within 2 steps of float32
+    if (i < p.count) {
+      const f32x2 rr = make2(rstd, rstd);
+      if constexpr (kKeepW) {
 #pragma unroll
-      for (int e = 0; e < kPairs; ++e) x[e] = fma2(mul2(x[e], rr), w[e], b[e]);
-    }
+        for (int e = 0; e < kPairs; ++e) x[e] = fma2(mul2(x[e], rr), w[e], b[e]);
+      }
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int c = (n * A.lanes + p.lane) * V;
-      if (c < A.D) {
-        if constexpr (!kKeepW) {
-          f32x2 wp[V / 2], bp[V / 2];
-          params<V>(A.w, static_cast<long long>(p.g) * A.D + c, 1.f, wp, 0);
-          params<V>(A.b, static_cast<long long>(p.g) * A.D + c, 0.f, bp, 0);
+      for (int n = 0; n < NV; ++n)
+        if (n * stride < left) {
+          if constexpr (!kKeepW) {
+            f32x2 wp[V / 2], bp[V / 2];
+            params<V>(A.w, gc + n * stride, 1.f, wp, 0);
+            params<V>(A.b, gc + n * stride, 0.f, bp, 0);
 #pragma unroll
-          for (int e = 0; e < V / 2; ++e) x[n * V / 2 + e] = fma2(mul2(x[n * V / 2 + e], rr), wp[e], bp[e]);
+            for (int e = 0; e < V / 2; ++e) x[n * V / 2 + e] = fma2(mul2(x[n * V / 2 + e], rr), wp[e], bp[e]);
+          }
+          Piece<T, V>::put(out + n * stride, x, n * V);
         }
-        Piece<T, V>::put(out + c, x, n * V);
+      if (p.lane == 0) {
+        if (A.mean != nullptr) A.mean[stat] = mean;
+        if (A.rstd != nullptr) A.rstd[stat] = rstd;
       }
     }
-    if (p.lane == 0) {
-      if (A.mean != nullptr) A.mean[m * A.G + p.g] = mean;
-      if (A.rstd != nullptr) A.rstd[m * A.G + p.g] = rstd;
-    }
+    out += jump;
+    stat += static_cast<long long>(p.step) * A.G;
   }
 }
 
@@ -301,28 +304,31 @@ __global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(backwa
   pdl_wait();
   pdl_trigger();
   const Place p = place<kBlock>(A);
-  const int warps = warps_pow2();
+  const int warps = warps_pow2(), stride = A.lanes * V, left = A.D - p.lane * V;
   const float inv = 1.f / static_cast<float>(A.D);
+  const long long gc = static_cast<long long>(p.g) * A.D + p.lane * V, jump = row_step(A, p);
   f32x2 w[kPairs] = {}, aw[kPairs] = {}, ab[kPairs] = {};
 #pragma unroll
-  for (int n = 0; n < NV; ++n) {
-    const int c = (n * A.lanes + p.lane) * V;
-    if (p.active && c < A.D) params<V>(A.w, static_cast<long long>(p.g) * A.D + c, 1.f, w, n * V);
-  }
-  const long long rows = (A.M + p.step - 1) / p.step;
+  for (int n = 0; n < NV; ++n)
+    if (p.count > 0 && n * stride < left) params<V>(A.w, gc + n * stride, 1.f, w, n * V);
+  const T *inx = A.x + first_at(A, p, V), *ind = A.dy + first_at(A, p, V);
+  T *out = A.out + first_at(A, p, V);
+  long long stat = static_cast<long long>(p.m0) * A.G + p.g;
   Piece<T, V> nx[NV], nd[NV];
   float nmean = 0.f, nrstd = 0.f;
-  auto fetch_all = [&](long long m) {
-    fetch(A, A.x, p, m, nx);
-    fetch(A, A.dy, p, m, nd);
-    if (p.active && m < A.M) {
-      nmean = A.mean[m * A.G + p.g];
-      nrstd = A.rstd[m * A.G + p.g];
+  auto fetch_all = [&](bool on) {
+    fetch(inx, on, stride, left, nx);
+    fetch(ind, on, stride, left, nd);
+    if (on) {
+      nmean = A.mean[stat];
+      nrstd = A.rstd[stat];
     }
+    inx += jump;
+    ind += jump;
+    stat += static_cast<long long>(p.step) * A.G;
   };
-  fetch_all(p.m);
-  for (long long i = 0; i < rows; ++i) {
-    const long long m = p.m + i * p.step;
+  fetch_all(p.count > 0);
+  for (int i = 0; i < p.turns; ++i) {
     Piece<T, V> ux[NV], ud[NV];
     const float rstd = nrstd;
     const f32x2 rr = make2(rstd, rstd), mm = make2(-nmean, -nmean);
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(backwa
       ux[n] = nx[n];
       ud[n] = nd[n];
     }
-    fetch_all(m + p.step);
+    fetch_all(i + 1 < p.count);
     f32x2 sg = make2(0.f, 0.f), sx = make2(0.f, 0.f);  // sums of g and g xh
     // (past the vector's end dy is zero, and so is what it adds)
     {
@@ -354,45 +360,40 @@ __global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(backwa
     split2(sg, a, b);
     split2(sx, c0, d0);
     const float2 s = unit_sum<kBlock>(make_float2(a + b, c0 + d0), A.lanes, warps, red, turn);
-    if (!(p.active && m < A.M)) continue;
-    // dx = rstd (g - mg - xh mgx)
-    const float mg = -s.x * inv * rstd, mgx = -s.y * inv * rstd;
-    const f32x2 mg2 = make2(mg, mg), mgx2 = make2(mgx, mgx);
-    T *out = A.out + (m * A.G + p.g) * A.D;
-    f32x2 x[kPairs] = {}, d[kPairs] = {};
+    if (i < p.count) {
+      // dx = rstd (g - mg - xh mgx)
+      const float mg = -s.x * inv * rstd, mgx = -s.y * inv * rstd;
+      const f32x2 mg2 = make2(mg, mg), mgx2 = make2(mgx, mgx);
+      f32x2 x[kPairs] = {}, d[kPairs] = {};
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      ux[n].get(x, n * V);
-      ud[n].get(d, n * V);
+      for (int n = 0; n < NV; ++n) {
+        ux[n].get(x, n * V);
+        ud[n].get(d, n * V);
+      }
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e)
+        d[e] = fma2(mul2(d[e], w[e]), rr, fma2(mul2(add2(x[e], mm), rr), mgx2, mg2));
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        if (n * stride < left) Piece<T, V>::put(out + n * stride, d, n * V);
     }
-#pragma unroll
-    for (int e = 0; e < kPairs; ++e)
-      d[e] = fma2(mul2(d[e], w[e]), rr, fma2(mul2(add2(x[e], mm), rr), mgx2, mg2));
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int c = (n * A.lanes + p.lane) * V;
-      if (c < A.D) Piece<T, V>::put(out + c, d, n * V);
-    }
+    out += jump;
   }
   if (A.partial == nullptr) return;
   // this CTA's sums: over its units of each group, in order
   const long long GD = static_cast<long long>(A.G) * A.D;
-  float *out = A.partial + (blockIdx.x / A.gblocks) * 2 * GD;
+  float *part = A.partial + (blockIdx.x / A.gblocks) * 2 * GD;
   if (kBlock || A.slots == 1) {
+    constexpr int kF = V % 4 == 0 ? 4 : 1;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-      const int c = (n * A.lanes + p.lane) * V;
-      if (p.active && c < A.D) {
-        const long long pc = static_cast<long long>(p.g) * A.D + c;
-        Piece<float, V % 4 == 0 ? 4 : 1>::put(out + pc, aw, n * V);
-        Piece<float, V % 4 == 0 ? 4 : 1>::put(out + GD + pc, ab, n * V);
+    for (int n = 0; n < NV; ++n)
+      if (p.g < A.G && n * stride < left) {
 #pragma unroll
-        for (int e = V % 4 == 0 ? 4 : 1; e < V; e += V % 4 == 0 ? 4 : 1) {
-          Piece<float, V % 4 == 0 ? 4 : 1>::put(out + pc + e, aw, n * V + e);
-          Piece<float, V % 4 == 0 ? 4 : 1>::put(out + GD + pc + e, ab, n * V + e);
+        for (int e = 0; e < V; e += kF) {
+          Piece<float, kF>::put(part + gc + n * stride + e, aw, n * V + e);
+          Piece<float, kF>::put(part + GD + gc + n * stride + e, ab, n * V + e);
         }
       }
-    }
     return;
   }
   const int width = A.gper * A.lanes * NV * V, slot = p.unit / A.gper, col0 = (p.unit % A.gper) * A.lanes * NV * V;
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(backwa
     if (g >= A.G || c >= A.D) continue;
     float t = 0.f;
     for (int s = 0; s < A.slots; ++s) t += sums[(which * A.slots + s) * width + col];
-    out[which * GD + static_cast<long long>(g) * A.D + c] = t;
+    part[which * GD + static_cast<long long>(g) * A.D + c] = t;
   }
 }
 
@@ -434,7 +435,7 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_long_ke
     q = fmaf(d, d, q);
   }
   const float var = unit_sum<true>(q, 32, 32, red, turn) / static_cast<float>(A.D);
-  const float rstd = 1.f / sqrtf(var + A.eps);
+  const float rstd = rsqrtf(var + A.eps);
   for (int c = threadIdx.x; c < A.D; c += blockDim.x) {
     const float xh = (Elem<T>::load(A.x + base + c) - mean) * rstd;
     Elem<T>::store(A.out + base + c, fmaf(xh, A.w ? A.w[gc + c] : 1.f, A.b ? A.b[gc + c] : 0.f));
