@@ -428,10 +428,15 @@ def _device_of(t, name: str):
     return t.device
 
 
+# the handle of a device's current stream; torch's own shortcut takes 0.1 us, the public way 2.2 us
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call_on(device, stream, name: str, *args) -> None:
     """The entry point on a stream of the tensors' device, which need not be the current one."""
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
+        stream = _current_stream(device.index)
     elif isinstance(stream, torch.cuda.Stream):
         if stream.device != device:
             raise ValueError(f"a stream of {stream.device} for tensors on {device}")
@@ -445,11 +450,14 @@ def _call_on(device, stream, name: str, *args) -> None:
             _call(name, *args, stream)
 
 
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
 def _on(stream, device):
     """Where a convenience allocates: on the stream that its kernels run on, so that nothing it frees
     is handed out again before they are done."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE_AND_NOW
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
@@ -773,7 +781,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, *, grouped=False, stream=Non
             _fits_or_none(bias, "bias", f32, p, dev))
     with _on(stream, dev):
         y = torch.empty_like(x)
-        mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+        mean = x.new_empty(shape[:-1], dtype=f32)
         rstd = torch.empty_like(mean)
     _call_on(dev, stream, "rwkv7_layer_norm" if f32_x else "rwkv7_layer_norm_bf16", M, G, D, float(eps), *args,
              y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
@@ -792,7 +800,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, grouped=False, stream=None
     n = load_library().rwkv7_layer_norm_workspace(0 if f32_x else 1, M, G, D)
     with _on(stream, dev):
         dx = torch.empty_like(x)
-        dweight = torch.empty(p, dtype=f32, device=dev)
+        dweight = x.new_empty(p, dtype=f32)
         dbias = torch.empty_like(dweight)
         ws = _workspace(n, dev)
     _call_on(dev, stream, "rwkv7_layer_norm_backward" if f32_x else "rwkv7_layer_norm_backward_bf16", M, G, D, *args,

@@ -33,7 +33,7 @@ struct Shape {
   long long total_T;
   int H;
   int nseg;     // segments per sequence (1: the whole sequence)
-  int seg_len;  // tokens per segment, a multiple of 128; the last segment runs to the sequence's end
+  int seg_len;  // tokens per segment (on the tensor cores whole chunks); the last segment runs to the sequence's end
 };
 
 // Tokens lo .. lo + len - 1 of the packed operands; `first` / `last`: this segment begins / ends the
@@ -70,6 +70,43 @@ __device__ __forceinline__ double powi(double w, long long n) {
 // element (row, col) of a state as it is stored
 __device__ __forceinline__ int state_at(int transposed, int row, int col) {
   return transposed ? col * kN + row : row * kN + col;
+}
+
+// Launches a kernel that waits (pdl_wait) before it touches memory: its CTAs may be placed while the grid
+// before it on the stream drains.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_waiting(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream,
+                           const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// The batch row of a CTA: rows of a ragged batch are taken from the longest to the shortest (up to kMaxSorted
+// rows; equal ones in order), so that none is left to the end.  `lens`, kMaxSorted ints of shared memory and
+// one more.  Called by a whole CTA of at least kMaxSorted / 2 threads.
+constexpr int kMaxSorted = 256;
+__device__ __forceinline__ int sorted_row(const Shape &P, int b, int B, int *lens) {
+  if (P.cu_seqlens == nullptr || B > kMaxSorted) return b;
+  for (int i = threadIdx.x; i < B; i += blockDim.x) lens[i] = seq_bounds(P.cu_seqlens, i, P.T, P.total_T).len;
+  __syncthreads();
+  for (int i = threadIdx.x; i < B; i += blockDim.x) {
+    int before = 0;
+    const int len = lens[i];
+    for (int j = 0; j < B; ++j) before += lens[j] > len || (lens[j] == len && j < i);
+    if (before == b) lens[kMaxSorted] = i;
+  }
+  __syncthreads();
+  return lens[kMaxSorted];
 }
 
 }  // namespace lin

@@ -22,9 +22,11 @@ template <typename TIn> bool use_chunk(long long max_T) { return sizeof(TIn) == 
 
 // Segments a sequence of at most T tokens is split into, for `chains` sequences that run side by side: as
 // many as fill the CTAs that the device runs at once (2 per SM on the tensor cores, 4 of the
-// token-by-token kernel).
+// token-by-token kernel), of at least one chunk, or of 64 tokens (token by token, B1 T1000 H12 float32:
+// 90 us with segments of 256 tokens, @@ with 64).
+int unit(bool chunk) { return chunk ? 128 : 64; }
 int segments(long long chains, long long T, bool chunk) {
-  const long long want = (chunk ? 296 : 592) / chains, most = T / 128;
+  const long long want = (chunk ? 296 : 592) / chains, most = T / unit(chunk);
   const long long n = want < most ? want : most;
   return n < 1 ? 1 : static_cast<int>(n);
 }
@@ -45,7 +47,7 @@ lin::Shape shape(const float *w, const int32_t *cu, int B, int T, long long tota
   int n = segments(passes * pairs, max_T, chunk);
   const long long room = bytes / (passes * pairs * kStateBytes);
   if (n > room) n = room < 2 ? 1 : static_cast<int>(room);
-  const long long len = (((max_T + n - 1) / n) + 127) / 128 * 128;
+  const long long u = chunk ? unit(true) : 16, len = ((max_T + n - 1) / n + u - 1) / u * u;
   if (n > 1) n = static_cast<int>((max_T + len - 1) / len);
   return lin::Shape{w, cu, T, total_T, H, n, n > 1 ? static_cast<int>(len) : 0x7fffff80};
 }

@@ -120,11 +120,11 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t sr
 
 // One segment of one pass.
 template <bool kRev, bool kOut>
-__device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, const Shape &P, int z,
+__device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, const Shape &P, int b, int z,
                                      uint8_t *smem_raw, int *err_word) {
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;  // shared-memory addresses from here on
   uint8_t *smem = smem_raw + (sm - smem_u32(smem_raw));
-  const int h = blockIdx.x, b = blockIdx.y;
+  const int h = blockIdx.x;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const bool elected = elect_one();
   const Segment sg = segment(P, b, z);
@@ -476,12 +476,15 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_chunk_kernel(const __grid
                                                                     const __grid_constant__ Passes<uint16_t> A,
                                                                     const Shape P, int *err_word) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ int lens[kMaxSorted + 1];
   pdl_wait();
+  pdl_trigger();
+  const int b = sorted_row(P, blockIdx.y, gridDim.y, lens);
   const int nz = kOut ? P.nseg : P.nseg - 1, role = blockIdx.z / nz, z = blockIdx.z - role * nz;
   if (A.p[role].reverse)
-    walk<true, kOut>(maps.m[role], A.p[role], P, kOut ? z : z + 1, smem_raw, err_word);
+    walk<true, kOut>(maps.m[role], A.p[role], P, b, kOut ? z : z + 1, smem_raw, err_word);
   else
-    walk<false, kOut>(maps.m[role], A.p[role], P, z, smem_raw, err_word);
+    walk<false, kOut>(maps.m[role], A.p[role], P, b, z, smem_raw, err_word);
 }
 
 using PFN_encodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -534,8 +537,7 @@ cudaError_t launch_linattn_chunk(const lin::Passes<uint16_t> &A, const lin::Shap
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemBytes));
     if (e != cudaSuccess) return e;
-    kern<<<dim3(P.H, B, nz * A.n), kThreads, kSmemBytes, stream>>>(maps, A, P, err_word);
-    return cudaGetLastError();
+    return launch_waiting(kern, dim3(P.H, B, nz * A.n), kThreads, kSmemBytes, stream, maps, A, P, err_word);
   };
   return A.state_only ? run(linattn_chunk_kernel<false>) : run(linattn_chunk_kernel<true>);
 }

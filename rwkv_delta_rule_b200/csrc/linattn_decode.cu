@@ -54,17 +54,8 @@ cudaError_t launch_linattn_decode(const TIn *r, const TIn *k, const TIn *v, cons
                                   int H, cudaStream_t stream) {
   const long long pairs = static_cast<long long>(B) * H;
   if (pairs > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, lin::linattn_decode_kernel<TIn>, r, k, v, w, s, y, H);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return lin::launch_waiting(lin::linattn_decode_kernel<TIn>, dim3(static_cast<unsigned>(pairs)), 256, 0, stream, r, k,
+                             v, w, s, y, H);
 }
 
 template cudaError_t launch_linattn_decode<float>(const float *, const float *, const float *, const float *, float *,

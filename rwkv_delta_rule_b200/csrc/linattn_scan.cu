@@ -32,11 +32,11 @@ __device__ __forceinline__ void stage(const Pass<TIn> &A, TIn *buf, long long to
 }
 
 template <typename TIn, bool kRev, bool kOut>
-__device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P, int z, uint8_t *smem_raw) {
+__device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P, int b, int z, uint8_t *smem_raw) {
   using C = Tile<TIn>;
   TIn *bufs = reinterpret_cast<TIn *>(smem_raw);
   float *ys = reinterpret_cast<float *>(smem_raw + 2 * C::kElems * sizeof(TIn));
-  const int h = blockIdx.x, b = blockIdx.y;
+  const int h = blockIdx.x;
   const Segment sg = segment(P, b, z);
   if (sg.len < 0) return;
   if (!kOut && (kRev ? sg.first : sg.last)) return;
@@ -75,7 +75,7 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
     }
     __syncthreads();
     const TIn *buf = bufs + (i & 1) * C::kElems;
-#pragma unroll 2
+#pragma unroll 4
     for (int u = 0; u < ntok; ++u) {
       const int tt = kRev ? ntok - 1 - u : u;
       const TIn *tk = buf + tt * 3 * kN;
@@ -141,12 +141,15 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
 template <typename TIn, bool kOut>
 __global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const __grid_constant__ Passes<TIn> A, const Shape P) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ int lens[kMaxSorted + 1];
   pdl_wait();
+  pdl_trigger();
+  const int b = sorted_row(P, blockIdx.y, gridDim.y, lens);
   const int nz = kOut ? P.nseg : P.nseg - 1, role = blockIdx.z / nz, z = blockIdx.z - role * nz;
   if (A.p[role].reverse)
-    scan_segment<TIn, true, kOut>(A.p[role], P, kOut ? z : z + 1, smem_raw);
+    scan_segment<TIn, true, kOut>(A.p[role], P, b, kOut ? z : z + 1, smem_raw);
   else
-    scan_segment<TIn, false, kOut>(A.p[role], P, z, smem_raw);
+    scan_segment<TIn, false, kOut>(A.p[role], P, b, z, smem_raw);
 }
 
 // One thread per 4 columns of a state row, along the segments.
@@ -155,6 +158,7 @@ template <typename TIn> __global__ void __launch_bounds__(256) linattn_join_kern
   const int h = blockIdx.x, b = blockIdx.y;
   const Pass<TIn> &A = passes.p[blockIdx.z >> 2];
   pdl_wait();
+  pdl_trigger();
   const SeqBounds sb = seq_bounds(P.cu_seqlens, b, P.T, P.total_T);
   if (sb.len < 0) return;
   const long long segs = (static_cast<long long>(sb.len) + P.seg_len - 1) / P.seg_len;
@@ -170,16 +174,25 @@ template <typename TIn> __global__ void __launch_bounds__(256) linattn_join_kern
                     f[state_at(A.s_in_t, row, col + 2)], f[state_at(A.s_in_t, row, col + 3)]);
   }
   float *ws = A.ws + pair * P.nseg * (kN * kN) + row * kN + col;
-  for (int i = 0; i < n; ++i) {
-    float4 *p = reinterpret_cast<float4 *>(ws + static_cast<long long>(A.reverse ? n - 1 - i : i) * (kN * kN));
-    if (i > 0) {
-      // the decay over the segment before; the sequence's last one may be of another length
-      float f = wl;
-      if (A.reverse && i == 1) f = static_cast<float>(powi(w, sb.len - static_cast<long long>(n - 1) * P.seg_len));
-      const float4 u = *p;
-      s = make_float4(fmaf(s.x, f, u.x), fmaf(s.y, f, u.y), fmaf(s.z, f, u.z), fmaf(s.w, f, u.w));
-    }
-    *p = s;
+  auto slot = [&](int i) {
+    return reinterpret_cast<float4 *>(ws + static_cast<long long>(A.reverse ? n - 1 - i : i) * (kN * kN));
+  };
+  *slot(0) = s;
+  // the slots in order, 8 loads at a time
+  for (int i0 = 1; i0 < n; i0 += 8) {
+    float4 u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i0 + j < n) u[j] = *slot(i0 + j);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i0 + j < n) {
+        // the decay over the segment before; the sequence's last one may be of another length
+        float f = wl;
+        if (A.reverse && i0 + j == 1) f = static_cast<float>(powi(w, sb.len - static_cast<long long>(n - 1) * P.seg_len));
+        s = make_float4(fmaf(s.x, f, u[j].x), fmaf(s.y, f, u[j].y), fmaf(s.z, f, u[j].z), fmaf(s.w, f, u[j].w));
+        *slot(i0 + j) = s;
+      }
   }
 }
 
@@ -191,17 +204,13 @@ cudaError_t launch_linattn_scan(const lin::Passes<TIn> &A, const lin::Shape &P, 
   const int nz = A.state_only ? P.nseg - 1 : P.nseg;
   if (nz <= 0) return cudaSuccess;
   const dim3 grid(P.H, B, nz * A.n);
-  if (A.state_only)
-    linattn_scan_kernel<TIn, false><<<grid, kThreads, Tile<TIn>::kSmem, stream>>>(A, P);
-  else
-    linattn_scan_kernel<TIn, true><<<grid, kThreads, Tile<TIn>::kSmem, stream>>>(A, P);
-  return cudaGetLastError();
+  return launch_waiting(A.state_only ? linattn_scan_kernel<TIn, false> : linattn_scan_kernel<TIn, true>, grid, kThreads,
+                        Tile<TIn>::kSmem, stream, A, P);
 }
 
 template <typename TIn>
 cudaError_t launch_linattn_join(const lin::Passes<TIn> &A, const lin::Shape &P, int B, cudaStream_t stream) {
-  lin::linattn_join_kernel<TIn><<<dim3(P.H, B, 4 * A.n), 256, 0, stream>>>(A, P);
-  return cudaGetLastError();
+  return lin::launch_waiting(lin::linattn_join_kernel<TIn>, dim3(P.H, B, 4 * A.n), 256, 0, stream, A, P);
 }
 
 template cudaError_t launch_linattn_scan<float>(const lin::Passes<float> &, const lin::Shape &, int, cudaStream_t);
