@@ -49,9 +49,7 @@ constexpr uint32_t TM_P = 0, TM_Y = 64, TM_YS = 128, TM_X = 192, kTmemCols = 256
 constexpr uint32_t OFF_Q = 0, OFF_K = kTile;
 constexpr uint32_t OFF_S = 2 * kTile;  // [64 value channels][64 key channels]; MMA1's rows behind K
 constexpr uint32_t OFF_V = OFF_S + kN * kN * 2, OFF_V1 = OFF_V + kTile, OFF_V2 = OFF_V1 + kTile, OFF_V3 = OFF_V2 + kTile;
-constexpr uint32_t OFF_CF = OFF_V3 + kTile;  // float [32]: w^(31-x), reversed w^x
-constexpr uint32_t OFF_ZERO = OFF_CF + 128;  // float [32]: zeros, the powers with negative exponents
-constexpr uint32_t OFF_PW = OFF_ZERO + 128;  // float [132]: w^n for n <= 128
+constexpr uint32_t OFF_PW = OFF_V3 + kTile;  // float [132]: w^n for n <= 128
 constexpr uint32_t OFF_PL = OFF_PW + 528;    // float [132]: what the rounding of w^n to float32 leaves
 constexpr uint32_t OFF_BAR = OFF_PL + 528;   // mbarriers, TMEM address, flags
 constexpr uint32_t kSmemBytes = OFF_BAR + 128 + 1024;
@@ -139,33 +137,25 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
 
   const int nchunks = (sg.len + kChunk - 1) / kChunk;
   auto chunk_at = [&](int i) { return kRev ? nchunks - 1 - i : i; };
-  // loads of chunk `it`, and the chunk after it on its way to L2
-  auto load_qk = [&](int it) {
-    const int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk, next = tok + (kRev ? -kChunk : kChunk);
-    tc::mbar_arrive_expect_tx(bars + B_QK, (kOut ? 2 : 1) * kTile);
-    tc::tma_load_3d(smem + OFF_K, &maps.k, bars + B_QK, 0, h, tok);
-    if (kOut) tc::tma_load_3d(smem + OFF_Q, &maps.q, bars + B_QK, 0, h, tok);
-    if (it + 1 < nchunks) {
-      tc::tma_prefetch_l2_3d(&maps.k, 0, h, next);
-      if (kOut) tc::tma_prefetch_l2_3d(&maps.q, 0, h, next);
-    }
+  // one tile of chunk `it`, and that of the chunk after it on its way to L2
+  auto load = [&](const CUtensorMap *map, uint32_t to, int bar, int it) {
+    const int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk;
+    tc::mbar_arrive_expect_tx(bars + bar, kTile);
+    tc::tma_load_3d(smem + to, map, bars + bar, 0, h, tok);
+    if (it + 1 < nchunks) tc::tma_prefetch_l2_3d(map, 0, h, tok + (kRev ? -kChunk : kChunk));
   };
-  auto load_v = [&](int it) {
-    const int tok = static_cast<int>(sg.lo) + chunk_at(it) * kChunk, next = tok + (kRev ? -kChunk : kChunk);
-    tc::mbar_arrive_expect_tx(bars + B_V, kTile);
-    tc::tma_load_3d(smem + OFF_V, &maps.v, bars + B_V, 0, h, tok);
-    if (it + 1 < nchunks) tc::tma_prefetch_l2_3d(&maps.v, 0, h, next);
-  };
-  constexpr int kLead = kRev ? 3 : 4;  // its rows have no products, or one group of them
+  // issues loads and MMAs; of the two warps of its rows the one without products of its own in P
+  constexpr int kLead = kRev ? 3 : 4;
   if (warp == kLead) {
     if (elected) {
-      for (int i = 0; i < kBars; ++i) tc::mbar_init(bars + i, i >= B_READY && i <= B_P ? 8 : 1);
+      for (int i = 0; i < kBars; ++i) tc::mbar_init(bars + i, i == B_READY || i == B_SPLIT ? 8 : i == B_P ? 7 : i == B_QK && kOut ? 2 : 1);
       tc::fence_mbar_init();
       *bad = 0;
       *stop = 0;
       if (nchunks > 0) {
-        load_v(0);
-        load_qk(0);
+        load(&maps.k, OFF_K, B_QK, 0);
+        if (kOut) load(&maps.q, OFF_Q, B_QK, 0);
+        load(&maps.v, OFF_V, B_V, 0);
       }
     }
     __syncwarp();
@@ -173,15 +163,12 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     tc::tmem_relinquish();
   }
   {
-    float *cf = reinterpret_cast<float *>(smem + OFF_CF), *pw = reinterpret_cast<float *>(smem + OFF_PW);
-    float *pl = reinterpret_cast<float *>(smem + OFF_PL);
-    if (tid < 32) reinterpret_cast<float *>(smem + OFF_ZERO)[tid] = 0.f;
+    float *pw = reinterpret_cast<float *>(smem + OFF_PW), *pl = reinterpret_cast<float *>(smem + OFF_PL);
     for (int n = tid; n <= kChunk; n += kThreads) {
       const double p = powi(static_cast<double>(P.w[h]), n);
       const float f = static_cast<float>(p);
       pw[n] = f;
       pl[n] = static_cast<float>(p - static_cast<double>(f));
-      if (n < 32) cf[kRev ? n : 31 - n] = f;
     }
   }
 
@@ -226,6 +213,8 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     return false;
   };
 
+  const float w1 = lds32(sm + OFF_PW + 4);
+  const f32x2 w2 = make2(w1 * w1, w1 * w1);
   // phases under way, for the leading lane to wait out if it has to give up
   int begun[kBars] = {};
   if (nchunks > 0) begun[B_QK] = begun[B_V] = 1;
@@ -256,10 +245,6 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
           tc::mma_commit(bars + B_M1);
           ++begun[B_M1];
         }
-        if (elected && it > 0) {
-          bulk_wait_read();
-          tc::mbar_arrive(bars + B_OUT);
-        }
         __syncwarp();
       }
     }
@@ -273,14 +258,15 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     {
       const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? row + 1 : max(L - 1 - row, 0)));
       const f32x2 f = make2(f1, f1);
-      uint32_t p1[4][4];
+      uint32_t in[4][4], p1[4][4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) lds128((at ^ (16 * x)) + OFF_V, in[x]);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        uint32_t in[4], p2[4], p3[4];
-        lds128((at ^ (16 * x)) + OFF_V, in);
+        uint32_t p2[4], p3[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const f32x2 v = mul2(make2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), f);
+          const f32x2 v = mul2(unpack2(in[x][e]), f);
           p1[x][e] = high_halves(v);
           const f32x2 r = sub2(v, cut2(v));
           p2[e] = high_halves(r);
@@ -289,7 +275,13 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
         sts128((at ^ (16 * x)) + OFF_V2, p2);
         sts128((at ^ (16 * x)) + OFF_V3, p3);
       }
-      if (kOut && it > 0) wait(B_OUT, it - 1);
+      if (kOut && it > 0) {
+        if (warp == kLead && elected) {
+          bulk_wait_read();
+          tc::mbar_arrive(bars + B_OUT);
+        }
+        wait(B_OUT, it - 1);
+      }
 #pragma unroll
       for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + OFF_V1, p1[x]);
     }
@@ -314,50 +306,62 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     if (kOut) {
       wait(B_M1, it);
       tc::tc_fence_after();
-      // P: column groups half and half + 2, 32 columns each.  Both halves' warps have read their
-      // products before either overwrites columns.
-      float pk[2][16];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int g = half + 2 * n;
-        if (g == rb) {
-          // w^(t-s), or zero past the diagonal: powers with 32 zeros in front
-          float v[32];
-          tc::tmem_ld32(tml + TM_P + 32 * g, v);
-          const uint32_t d = sm + OFF_PW + (kRev ? -4 * lane : 4 * lane);
-#pragma unroll
-          for (int x = 0; x < 16; ++x)
-            pk[n][x] = __uint_as_float(pack2(mul2(make2(v[2 * x], v[2 * x + 1]),
-                                                  make2(lds32(d + (kRev ? 8 * x : -8 * x)),
-                                                        lds32(d + (kRev ? 8 * x + 4 : -8 * x - 4))))));
-        } else if (kRev ? g > rb : g < rb) {
-          // w^(t-s) = w^(t - 32 g - 31) w^(31 - x), reversed w^(s-t) = w^(32 g - t) w^x
-          float v[32];
-          tc::tmem_ld32(tml + TM_P + 32 * g, v);
-          const float a1 = lds32(sm + OFF_PW + 4 * (kRev ? 32 * g - row : row - 32 * g - 31));
-          const f32x2 a = make2(a1, a1);
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            uint32_t f[4];
-            lds128(sm + OFF_CF + 16 * x, f);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              pk[n][2 * x + e] = __uint_as_float(
-                  pack2(mul2(make2(v[4 * x + 2 * e], v[4 * x + 2 * e + 1]),
-                             mul2(make2(__uint_as_float(f[2 * e]), __uint_as_float(f[2 * e + 1])), a))));
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 16; ++x) pk[n][x] = 0.f;
-        }
+      if (warp == kLead && elected && it + 1 < nchunks && !*bad) {
+        load(&maps.q, OFF_Q, B_QK, it + 1);
+        ++begun[B_QK];
       }
-      named_sync(1 + rb, 64);
-      tc::tmem_st16(tml + TM_P + 16 * half, pk[0]);
-      tc::tmem_st16(tml + TM_P + 16 * (half + 2), pk[1]);
-      tc::tmem_st_wait();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bars + B_P);
+      // P by column groups of 32: half and half + 2 for a warp, but all four for the lead's partner.  Both
+      // warps of the rows have read their products before either overwrites columns.
+      if (warp != kLead) {
+        const bool alone = rb == (kLead & 3);
+        float pk[2][16];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int g = half + 2 * n;
+          // (the powers come from repeated products: tables in shared memory had to wait for MMA3, which
+          // takes nearly all of its bandwidth meanwhile)
+          if (g == rb) {
+            // w^(t-s), zero past the diagonal: 1 on it, then a factor w per column
+            float v[32], f = 0.f;
+            tc::tmem_ld32(tml + TM_P + 32 * g, v);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const int e = kRev ? x : 31 - x;
+              f = e == lane ? 1.f : f * w1;
+              v[e] *= f;
+            }
+#pragma unroll
+            for (int x = 0; x < 16; ++x) pk[n][x] = __uint_as_float(pack2(make2(v[2 * x], v[2 * x + 1])));
+          } else if (kRev ? g > rb : g < rb) {
+            // w^(t-s) = w^(t - 32 g - 31) w^(31 - x), reversed w^(s-t) = w^(32 g - t) w^x
+            float v[32];
+            tc::tmem_ld32(tml + TM_P + 32 * g, v);
+            const float a = lds32(sm + OFF_PW + 4 * (kRev ? 32 * g - row : row - 32 * g - 31));
+            f32x2 f = kRev ? make2(a, a * w1) : make2(a * w1, a);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const int e = kRev ? x : 15 - x;
+              pk[n][e] = __uint_as_float(pack2(mul2(make2(v[2 * e], v[2 * e + 1]), f)));
+              f = mul2(f, w2);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) pk[n][x] = 0.f;
+          }
+        }
+        if (!alone) named_sync(1 + rb, 64);
+        tc::tmem_st16(tml + TM_P + 16 * half, pk[0]);
+        tc::tmem_st16(tml + TM_P + 16 * (half + 2), pk[1]);
+        if (alone) {
+          const float none[16] = {};
+          tc::tmem_st16(tml + TM_P + 16 * (half ^ 1), none);
+          tc::tmem_st16(tml + TM_P + 16 * ((half ^ 1) + 2), none);
+        }
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bars + B_P);
+      }
       if (warp == kLead) {
         if (wait(B_P, it) && elected) {
           tc::tc_fence_after();
@@ -377,10 +381,10 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     wait(B_M3, it);
     tc::tc_fence_after();
     if (warp == kLead && elected && it + 1 < nchunks && !*bad) {
-      load_qk(it + 1);
-      ++begun[B_QK];
+      load(&maps.k, OFF_K, B_QK, it + 1);
       if (!kOut) {
-        load_v(it + 1);
+        ++begun[B_QK];
+        load(&maps.v, OFF_V, B_V, it + 1);
         ++begun[B_V];
       }
     }
@@ -402,7 +406,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
       wait(B_M2, it);
       tc::tc_fence_after();
       if (warp == kLead && elected && it + 1 < nchunks && !*bad) {
-        load_v(it + 1);
+        load(&maps.v, OFF_V, B_V, it + 1);
         ++begun[B_V];
       }
       tc::tmem_ld32(tml + TM_Y + 32 * half, v);
