@@ -487,26 +487,46 @@ template <typename T> __global__ void __launch_bounds__(256) layer_norm_columns_
   A.partial[(blockIdx.x * 2 + 1) * GD + c] = ab;
 }
 
-// dw and db from the partial sums [n][2][GD]: 32 columns and 32 slices of n per CTA.
-__global__ void __launch_bounds__(1024) layer_norm_reduce_kernel(const float *partial, int n, long long GD, float *dw,
-                                                                float *db) {
-  __shared__ float part[32][33];
+// dw and db from the partial sums [n][2][GD]: 8 columns and 128 slices of n per CTA.
+__global__ void __launch_bounds__(256) layer_norm_reduce_kernel(const float *partial, int n, long long GD, float *dw,
+                                                               float *db) {
+  __shared__ float4 part[2][8];
   pdl_wait();
   pdl_trigger();
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const long long c = static_cast<long long>(blockIdx.x) * 32 + tx;
-  float t = 0.f;
-  if (c < 2 * GD) {
+  const int tx = threadIdx.x & 1, ty = threadIdx.x >> 1;
+  const long long cols = 2 * GD, c = static_cast<long long>(blockIdx.x) * 8 + 4 * tx;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  if ((cols & 3) == 0 && c < cols) {
 #pragma unroll 8
-    for (int i = ty; i < n; i += 32) t += partial[i * 2 * GD + c];
+    for (int i = ty; i < n; i += 128) {
+      const float4 u = *reinterpret_cast<const float4 *>(partial + i * cols + c);
+      t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+    }
+  } else {
+    for (int i = ty; i < n; i += 128) {
+      const float *p = partial + i * cols + c;
+      if (c < cols) t.x += p[0];
+      if (c + 1 < cols) t.y += p[1];
+      if (c + 2 < cols) t.z += p[2];
+      if (c + 3 < cols) t.w += p[3];
+    }
   }
-  part[ty][tx] = t;
-  __syncthreads();
-  t = part[tx][ty];
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-  const long long o = static_cast<long long>(blockIdx.x) * 32 + ty;
-  if (tx == 0 && o < 2 * GD) (o < GD ? dw[o] : db[o - GD]) = t;
+  for (int off = 16; off >= 2; off >>= 1) {
+    t.x += __shfl_xor_sync(0xffffffffu, t.x, off);
+    t.y += __shfl_xor_sync(0xffffffffu, t.y, off);
+    t.z += __shfl_xor_sync(0xffffffffu, t.z, off);
+    t.w += __shfl_xor_sync(0xffffffffu, t.w, off);
+  }
+  if ((threadIdx.x & 31) < 2) part[tx][threadIdx.x >> 5] = t;
+  __syncthreads();
+  if (threadIdx.x >= 8) return;
+  const float *q = reinterpret_cast<const float *>(part[threadIdx.x >> 2]) + (threadIdx.x & 3);
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += q[4 * i];
+  const long long o = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x;
+  if (o < cols) (o < GD ? dw[o] : db[o - GD]) = s;
 }
 
 // How the vectors are laid over lanes and CTAs.
@@ -652,7 +672,7 @@ cudaError_t launch_layer_norm_backward(const TIn *dy, const TIn *x, const float 
     if (e != cudaSuccess) return e;
   }
   if (dw == nullptr) return cudaSuccess;
-  return launch(layer_norm_reduce_kernel, dim3(ceil_div(2 * GD, 32)), 1024, 0, stream,
+  return launch(layer_norm_reduce_kernel, dim3(ceil_div(2 * GD, 8)), 256, 0, stream,
                 static_cast<const float *>(partial), M > 0 ? P.mblocks : 0, GD, dw, db);
 }
 

@@ -22,9 +22,9 @@ template <typename TIn> bool use_chunk(long long max_T) { return sizeof(TIn) == 
 
 // Segments a sequence of at most T tokens is split into, for `chains` sequences that run side by side: as
 // many as fill the CTAs that the device runs at once (2 per SM on the tensor cores, 4 of the
-// token-by-token kernel), of at least one chunk, or of 64 tokens (token by token, B1 T1000 H12 float32:
-// 90 us with segments of 256 tokens, @@ with 64).
-int unit(bool chunk) { return chunk ? 128 : 64; }
+// token-by-token kernel), of at least one chunk, or of 32 tokens (token by token, B1 T1000 H12 float32:
+// 90 us with segments of 256 tokens, 42 with 64, @@ with 32).
+int unit(bool chunk) { return chunk ? 128 : 32; }
 int segments(long long chains, long long T, bool chunk) {
   const long long want = (chunk ? 296 : 592) / chains, most = T / unit(chunk);
   const long long n = want < most ? want : most;

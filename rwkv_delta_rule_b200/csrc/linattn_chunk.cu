@@ -154,8 +154,8 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
       *stop = 0;
       if (nchunks > 0) {
         load(&maps.k, OFF_K, B_QK, 0);
-        if (kOut) load(&maps.q, OFF_Q, B_QK, 0);
         load(&maps.v, OFF_V, B_V, 0);
+        if (kOut) load(&maps.q, OFF_Q, B_QK, 0);
       }
     }
     __syncwarp();
@@ -224,10 +224,12 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     // rows past the end hold other sequences' tokens: K and V count as zero there (Q's rows give
     // outputs that are not stored)
     const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+    // without outputs Q's tile is K's second one: the next K arrives while this one is in use
+    const uint32_t tile_k = !kOut && (it & 1) ? OFF_Q : OFF_K;
     wait(B_QK, it);
     if (row >= L) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + OFF_K, zero);
+      for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + tile_k, zero);
     }
     if (kOut) {
       tc::fence_proxy_async_smem();
@@ -296,9 +298,17 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
 #pragma unroll
         for (int ks = 0; ks < 24; ++ks)
           tc::mma_ss(0, tmem + TM_X, tc::smem_desc(sm + OFF_V1 + ks * 2048, kTile, 1024),
-                     tc::smem_desc(sm + OFF_K + (ks & 7) * 2048, kTile, 1024), d3, ks > 0);
+                     tc::smem_desc(sm + tile_k + (ks & 7) * 2048, kTile, 1024), d3, ks > 0);
         tc::mma_commit(bars + B_M3);
         ++begun[B_M3];
+        if (!kOut && it + 1 < nchunks && !*bad) {
+          // every warp is through with V and with its wait for this K, and MMA3 of the chunk before with the
+          // other one
+          load(&maps.k, OFF_Q + OFF_K - tile_k, B_QK, it + 1);
+          load(&maps.v, OFF_V, B_V, it + 1);
+          ++begun[B_QK];
+          ++begun[B_V];
+        }
       }
       __syncwarp();
     }
@@ -380,14 +390,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     // the state behind this chunk
     wait(B_M3, it);
     tc::tc_fence_after();
-    if (warp == kLead && elected && it + 1 < nchunks && !*bad) {
-      load(&maps.k, OFF_K, B_QK, it + 1);
-      if (!kOut) {
-        ++begun[B_QK];
-        load(&maps.v, OFF_V, B_V, it + 1);
-        ++begun[B_V];
-      }
-    }
+    if (kOut && warp == kLead && elected && it + 1 < nchunks && !*bad) load(&maps.k, OFF_K, B_QK, it + 1);
     {
       f32x2 x[8];
       tmem_ld_16x32(tml + TM_X + 32 * half, x);

@@ -297,3 +297,22 @@ def test_guard_bands():
     for buf in [b for b, _ in bufs] + [wbuf]:
         assert bool((buf[:pad] == 3.0).all()) and bool((buf[-pad:] == 3.0).all())
     ref.check_mix(y, s, r, k, v, w, st)
+
+
+@pytest.mark.parametrize("T", [1500, 2048])
+def test_many_chains_in_segments_of_several_chunks(T):
+    """96 chains in 3 segments of 4 to 6 chunks each: several CTAs per SM, forward and backward."""
+    r, k, v, w, dy, st, ds = inputs(3, T, 32, 23, torch.bfloat16)
+    assert lib7.rwkv7_linattn_workspace(3, T, 32) >= 3 * 96 * 64 * 64 * 4
+    y, s = lib7.linattn_prefill(r, k, v, w, st)
+    done()
+    ref.check_mix(y, s, r, k, v, w, st)
+    r, k, v, dy, st, ds = (x[:1].contiguous() for x in (r, k, v, dy, st, ds))  # 3 passes of 32 chains
+    grads = torch.full((3 * 3 * 32 * 64 * 64,), float("nan"), device="cuda")
+    dr, dk, dv, dsi = (torch.full_like(x, float("nan")) for x in (r, r, r, st))
+    lib7.rwkv7_linattn_backward_bf16(r, k, v, w, st, dy, ds, dr, dk, dv, dsi, grads)
+    done()
+    t = lambda x: x.transpose(-1, -2)  # noqa: E731
+    ref.check_mix(dr, None, dy, v, k, w, t(st), what="dr")
+    ref.check_mix(dk, None, v, dy, r, w, t(ds), reverse=True, what="dk")
+    ref.check_mix(dv, dsi, k, r, dy, w, ds, reverse=True, what="dv")
