@@ -18,7 +18,7 @@
 //     MMA1  [128 x 192] = Q [K; S0]^T                K-major tiles, as TMA and the warps left them
 //     MMA2  [128 x 64]  = P V                        P from TMEM in bf16, V as TMA left it (MN-major)
 //     MMA3  [64 x 64]   = V1 K + V2 K + V3 K         V1 + V2 + V3 = w^(L-1-s) v_s, MN-major
-// MMA3 and the new state run beside P and MMA2, and Q and K of the next chunk arrive meanwhile.
+// MMA3 and the new state run beside P and MMA2, and the tiles of the next chunk arrive meanwhile.
 // The state stays in float32 registers across chunks (16 elements per thread).  Roundings to bf16:
 //   P: one per product, as large as the rounding of out itself, and averaged over the tokens;
 //   S0 in MMA1: once, 2^-8 at most like P; it reaches out only.  A second term cost the 8 KB and the 64
@@ -224,12 +224,16 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     // rows past the end hold other sequences' tokens: K and V count as zero there (Q's rows give
     // outputs that are not stored)
     const uint32_t zero[4] = {0u, 0u, 0u, 0u};
-    // without outputs Q's tile is K's second one: the next K arrives while this one is in use
+    // The next V arrives in Q's tile once MMA1 is through with it, the next Q in V's behind MMA2, so the two
+    // change places from chunk to chunk.  Without outputs Q's tile is K's second one.
     const uint32_t tile_k = !kOut && (it & 1) ? OFF_Q : OFF_K;
-    wait(B_QK, it);
-    if (row >= L) {
+    const uint32_t tile_q = it & 1 ? OFF_V : OFF_Q, tile_v = kOut && (it & 1) ? OFF_Q : OFF_V;
+    if (L < kChunk) {
+      wait(B_QK, it);
+      if (row >= L) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + tile_k, zero);
+        for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + tile_k, zero);
+      }
     }
     if (kOut) {
       tc::fence_proxy_async_smem();
@@ -237,12 +241,12 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bars + B_READY);
       if (warp == kLead) {
-        if (wait(B_READY, it) && elected) {
+        if (wait(B_QK, it) && wait(B_READY, it) && elected) {
           tc::tc_fence_after();
           constexpr uint32_t d1 = tc::instr_desc(tc::kFmtBF16, 128, 192, false, false);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            tc::mma_ss(0, tmem + TM_P, tc::smem_desc(sm + OFF_Q + ks * 32, 16, 1024),
+            tc::mma_ss(0, tmem + TM_P, tc::smem_desc(sm + tile_q + ks * 32, 16, 1024),
                        tc::smem_desc(sm + OFF_K + ks * 32, 16, 1024), d1, ks > 0);
           tc::mma_commit(bars + B_M1);
           ++begun[B_M1];
@@ -255,14 +259,14 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     wait(B_V, it);
     if (row >= L) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + OFF_V, zero);
+      for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + tile_v, zero);
     }
     {
       const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? row + 1 : max(L - 1 - row, 0)));
       const f32x2 f = make2(f1, f1);
       uint32_t in[4][4], p1[4][4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) lds128((at ^ (16 * x)) + OFF_V, in[x]);
+      for (int x = 0; x < 4; ++x) lds128((at ^ (16 * x)) + tile_v, in[x]);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         uint32_t p2[4], p3[4];
@@ -292,7 +296,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(bars + B_SPLIT);
     if (warp == kLead) {
-      if (wait(B_SPLIT, it) && elected) {
+      if ((kOut || wait(B_QK, it)) && wait(B_SPLIT, it) && elected) {
         tc::tc_fence_after();
         constexpr uint32_t d3 = tc::instr_desc(tc::kFmtBF16, 64, 64, true, true);
 #pragma unroll
@@ -302,8 +306,8 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
         tc::mma_commit(bars + B_M3);
         ++begun[B_M3];
         if (!kOut && it + 1 < nchunks && !*bad) {
-          // every warp is through with V and with its wait for this K, and MMA3 of the chunk before with the
-          // other one
+          // every warp is through with V and with its waits for these tiles, and MMA3 of the chunk before with
+          // the other K
           load(&maps.k, OFF_Q + OFF_K - tile_k, B_QK, it + 1);
           load(&maps.v, OFF_V, B_V, it + 1);
           ++begun[B_QK];
@@ -317,8 +321,8 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
       wait(B_M1, it);
       tc::tc_fence_after();
       if (warp == kLead && elected && it + 1 < nchunks && !*bad) {
-        load(&maps.q, OFF_Q, B_QK, it + 1);
-        ++begun[B_QK];
+        load(&maps.v, tile_q, B_V, it + 1);
+        ++begun[B_V];
       }
       // P by column groups of 32: half and half + 2 for a warp, but all four for the lead's partner.  Both
       // warps of the rows have read their products before either overwrites columns.
@@ -378,7 +382,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
           constexpr uint32_t d2 = tc::instr_desc(tc::kFmtBF16, 128, 64, false, true);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            tc::mma_ts_bf16(tmem + TM_Y, tmem + TM_P + 8 * ks, tc::smem_desc(sm + OFF_V + ks * 2048, kTile, 1024), d2,
+            tc::mma_ts_bf16(tmem + TM_Y, tmem + TM_P + 8 * ks, tc::smem_desc(sm + tile_v + ks * 2048, kTile, 1024), d2,
                             ks > 0);
           tc::mma_commit(bars + B_M2);
           ++begun[B_M2];
@@ -390,7 +394,10 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     // the state behind this chunk
     wait(B_M3, it);
     tc::tc_fence_after();
-    if (kOut && warp == kLead && elected && it + 1 < nchunks && !*bad) load(&maps.k, OFF_K, B_QK, it + 1);
+    if (kOut && warp == kLead && elected && it + 1 < nchunks && !*bad) {
+      load(&maps.k, OFF_K, B_QK, it + 1);
+      ++begun[B_QK];
+    }
     {
       f32x2 x[8];
       tmem_ld_16x32(tml + TM_X + 32 * half, x);
@@ -408,10 +415,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
       tc::tmem_ld32(tml + TM_YS + 32 * half, y);
       wait(B_M2, it);
       tc::tc_fence_after();
-      if (warp == kLead && elected && it + 1 < nchunks && !*bad) {
-        load(&maps.v, OFF_V, B_V, it + 1);
-        ++begun[B_V];
-      }
+      if (warp == kLead && elected && it + 1 < nchunks && !*bad) load(&maps.q, tile_v, B_QK, it + 1);
       tc::tmem_ld32(tml + TM_Y + 32 * half, v);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
