@@ -196,6 +196,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
                                      from[state_at(t, i0 + 8 * (e & 1), j0 + 8 * (e >> 1) + 1)]);
     if (kOut) put_state();
   }
+  tc::fence_proxy_async_smem();
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -234,9 +235,9 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
 #pragma unroll
         for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + tile_k, zero);
       }
+      tc::fence_proxy_async_smem();
     }
     if (kOut) {
-      tc::fence_proxy_async_smem();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bars + B_READY);
@@ -425,9 +426,8 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
           u[e] = pack2(fma2(make2(y[8 * x + 2 * e], y[8 * x + 2 * e + 1]), f, make2(v[8 * x + 2 * e], v[8 * x + 2 * e + 1])));
         sts128((at ^ (16 * x)) + OFF_V1, u);
       }
-      if (L == kChunk) {
-        tc::fence_proxy_async_smem();
-      } else {
+      tc::fence_proxy_async_smem();  // the rows of out, and the state
+      if (L < kChunk) {
         // not the whole tile: the warp's 32 half rows, 4 lanes to each
         __syncwarp();
         const int r0 = 32 * rb + (lane >> 2), ch = 4 * half + (lane & 3);
