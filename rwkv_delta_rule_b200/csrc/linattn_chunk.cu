@@ -41,7 +41,7 @@ constexpr uint32_t kMaxPolls = 1u << 22;
 constexpr uint32_t kTile = kChunk * kN * 2;  // one bf16 128 x 64 tile, 128-byte swizzled rows
 
 // TMEM columns.  MMA1 fills 0 .. 191 (q k, then q S0); P (bf16 pairs) replaces the first 64 of the
-// products once they have been read, MMA2's result the second 64.  MMA3's 64 rows lie 16 to each warp's 32 lanes.
+// products as they are read, MMA2's result the second 64.  MMA3's 64 rows lie 16 to each warp's 32 lanes.
 constexpr uint32_t TM_P = 0, TM_Y = 64, TM_YS = 128, TM_X = 192, kTmemCols = 256;
 
 // shared memory, from a 1024-aligned base.  V1's tile is where the rows of out are put together for
@@ -146,6 +146,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
   };
   // issues loads and MMAs; of the two warps of its rows the one without products of its own in P
   constexpr int kLead = kRev ? 3 : 4;
+  constexpr int kStore = kRev ? 4 : 3;  // issues the TMA stores of out
   if (warp == kLead) {
     if (elected) {
       for (int i = 0; i < kBars; ++i) tc::mbar_init(bars + i, i == B_READY || i == B_SPLIT ? 8 : i == B_P ? 7 : i == B_QK && kOut ? 2 : 1);
@@ -265,32 +266,31 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     {
       const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? row + 1 : max(L - 1 - row, 0)));
       const f32x2 f = make2(f1, f1);
-      uint32_t in[4][4], p1[4][4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) lds128((at ^ (16 * x)) + tile_v, in[x]);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        uint32_t p2[4], p3[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const f32x2 v = mul2(unpack2(in[x][e]), f);
-          p1[x][e] = high_halves(v);
-          const f32x2 r = sub2(v, cut2(v));
-          p2[e] = high_halves(r);
-          p3[e] = high_halves(sub2(r, cut2(r)));
-        }
-        sts128((at ^ (16 * x)) + OFF_V2, p2);
-        sts128((at ^ (16 * x)) + OFF_V3, p3);
-      }
-      if (kOut && it > 0) {
-        if (warp == kLead && elected) {
+      if (kOut && it > 0) {  // V1's tile has been stored from
+        if (warp == kStore && elected) {
           bulk_wait_read();
           tc::mbar_arrive(bars + B_OUT);
         }
         wait(B_OUT, it - 1);
       }
+      uint32_t in[4];
+      lds128(at + tile_v, in);
+#pragma unroll 1
+      for (int x = 0; x < 64; x += 16) {
+        uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) sts128((at ^ (16 * x)) + OFF_V1, p1[x]);
+        for (int e = 0; e < 4; ++e) {
+          const f32x2 v = mul2(unpack2(in[e]), f);
+          p1[e] = high_halves(v);
+          const f32x2 r = sub2(v, cut2(v));
+          p2[e] = high_halves(r);
+          p3[e] = high_halves(sub2(r, cut2(r)));
+        }
+        if (x < 48) lds128((at ^ (x + 16)) + tile_v, in);
+        sts128((at ^ x) + OFF_V1, p1);
+        sts128((at ^ x) + OFF_V2, p2);
+        sts128((at ^ x) + OFF_V3, p3);
+      }
     }
     tc::fence_proxy_async_smem();
     tc::tc_fence_before();
@@ -325,16 +325,16 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
         load(&maps.v, tile_q, B_V, it + 1);
         ++begun[B_V];
       }
-      // P by column groups of 32: half and half + 2 for a warp, but all four for the lead's partner.  Both
-      // warps of the rows have read their products before either overwrites columns.
+      // P by column groups of 32: half and half + 2 for a warp, all four for the lead's partner.  P goes over
+      // products that this warp has read: group g to columns 32 (g % 2) + 16 (g / 2) .. + 15.
+      // (The powers come from repeated products: tables in shared memory had to wait for MMA3, which takes
+      // nearly all of its bandwidth meanwhile.)
       if (warp != kLead) {
-        const bool alone = rb == (kLead & 3);
-        float pk[2][16];
-#pragma unroll
+#pragma unroll 1
         for (int n = 0; n < 2; ++n) {
           const int g = half + 2 * n;
-          // (the powers come from repeated products: tables in shared memory had to wait for MMA3, which
-          // takes nearly all of its bandwidth meanwhile)
+          const uint32_t to = tml + TM_P + 32 * half + 16 * n;
+          float pk[16];
           if (g == rb) {
             // w^(t-s), zero past the diagonal: 1 on it, then a factor w per column
             float v[32], f = 0.f;
@@ -346,7 +346,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
               v[e] *= f;
             }
 #pragma unroll
-            for (int x = 0; x < 16; ++x) pk[n][x] = __uint_as_float(pack2(make2(v[2 * x], v[2 * x + 1])));
+            for (int x = 0; x < 16; ++x) pk[x] = __uint_as_float(pack2(make2(v[2 * x], v[2 * x + 1])));
           } else if (kRev ? g > rb : g < rb) {
             // w^(t-s) = w^(t - 32 g - 31) w^(31 - x), reversed w^(s-t) = w^(32 g - t) w^x
             float v[32];
@@ -356,21 +356,19 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
               const int e = kRev ? x : 15 - x;
-              pk[n][e] = __uint_as_float(pack2(mul2(make2(v[2 * e], v[2 * e + 1]), f)));
+              pk[e] = __uint_as_float(pack2(mul2(make2(v[2 * e], v[2 * e + 1]), f)));
               f = mul2(f, w2);
             }
           } else {
 #pragma unroll
-            for (int x = 0; x < 16; ++x) pk[n][x] = 0.f;
+            for (int x = 0; x < 16; ++x) pk[x] = 0.f;
           }
-        }
-        if (!alone) named_sync(1 + rb, 64);
-        tc::tmem_st16(tml + TM_P + 16 * half, pk[0]);
-        tc::tmem_st16(tml + TM_P + 16 * (half + 2), pk[1]);
-        if (alone) {
-          const float none[16] = {};
-          tc::tmem_st16(tml + TM_P + 16 * (half ^ 1), none);
-          tc::tmem_st16(tml + TM_P + 16 * ((half ^ 1) + 2), none);
+          tc::tmem_st16(to, pk);
+          if (rb == (kLead & 3)) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) pk[x] = 0.f;
+            tc::tmem_st16(tml + TM_P + 32 * (half ^ 1) + 16 * n, pk);
+          }
         }
         tc::tmem_st_wait();
         tc::tc_fence_before();
@@ -383,7 +381,8 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
           constexpr uint32_t d2 = tc::instr_desc(tc::kFmtBF16, 128, 64, false, true);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            tc::mma_ts_bf16(tmem + TM_Y, tmem + TM_P + 8 * ks, tc::smem_desc(sm + tile_v + ks * 2048, kTile, 1024), d2,
+            tc::mma_ts_bf16(tmem + TM_Y, tmem + TM_P + 32 * ((ks >> 1) & 1) + 16 * (ks >> 2) + 8 * (ks & 1),
+                            tc::smem_desc(sm + tile_v + ks * 2048, kTile, 1024), d2,
                             ks > 0);
           tc::mma_commit(bars + B_M2);
           ++begun[B_M2];
@@ -444,12 +443,12 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     if (tid == 0) *stop = *bad;
     named_sync(5, kThreads);
     if (*stop) break;
-    if (kOut && L == kChunk && warp == kLead && elected) {
+    if (kOut && L == kChunk && warp == kStore && elected) {
       tma_store_3d(&maps.out, sm + OFF_V1, 0, h, static_cast<int>(sg.lo) + c * kChunk);
       tc::bulk_commit_group();
     }
   }
-  if (kOut && warp == kLead && elected) tc::bulk_wait_all();
+  if (kOut && warp == kStore && elected) tc::bulk_wait_all();
   if (warp == kLead && elected && *bad) {
     // give up: whatever is still in flight lands first
     report_device_error(err_word, kDevErrTimeout);
