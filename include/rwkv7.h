@@ -383,6 +383,11 @@ RWKV7_API rwkv7_status rwkv7_wkv_backward_bf16(int B, int T, int H, int N, const
  * order.  The contents need no preparation and mean nothing afterwards; calls that may run at once
  * need workspaces of their own, replays of a captured call included.
  *
+ * bfloat16 calls of 32 tokens and more run in chunks of 128 tokens on the tensor cores: y is then off by
+ * its own rounding and by one bf16 rounding each of the products r_t . k_s and of the state a chunk begins
+ * with; the states keep float32 accuracy.  A NaN or an infinity among a sequence's operands reaches
+ * its later outputs, and there those of up to 127 tokens before it too; it never reaches another sequence.
+ *
  * varlen: cu_seqlens and max_T as for rwkv7_wkv_prefill_varlen_bf16.
  * backward: gradients of a loss with dL/dy = dy and dL/ds_out = ds_out (NULL: zero).  It needs the
  *   operands alone, no checkpoints: with G_t = dL/dS_t = dy_t r_t^T + w G_{t+1},

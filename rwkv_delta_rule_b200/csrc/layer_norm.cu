@@ -14,6 +14,11 @@
 // whole CTA.  A unit keeps its group g and steps over the rows m, so it also keeps its columns' sums
 // for dw and db in registers; CTAs then leave one partial sum each, and a second launch adds those up
 // in a fixed order.  Vectors too long for a CTA's registers are walked in loops instead.
+//
+// Measured on B200 (us, share of measured HBM): forward 65536 x 4096 bf16 197 to 201, 82 %; gradients
+// 16384 x 64 x 64 82, 76 %; 32768 x 768 37, 61 % (31 for the rows, 6 for the sum of the partials and the
+// launch between).  Steps that carried, for the forward: rows fetched ahead and weights in registers 288 to
+// 227, pointers instead of index arithmetic per row 227 to 201 (it was bound by its instructions).
 #include "layer_norm.h"
 
 #include "common.cuh"
@@ -198,7 +203,7 @@ __device__ __forceinline__ void fetch(const T *row, bool on, int stride, int lef
 // Registers a thread may take with E elements.  Forward: two float32 parameters (beyond 16 elements they
 // are read again from L1) and the value per element, and one or two rows fetched ahead: with rows of
 // 8 KB, 48 KB are in flight per SM.  Backward: the weight, two sums, and the row under way and the next of
-// two tensors.
+// two tensors (24 elements per lane spilled: 32768 x 768 took 73 us with one warp per row, 39 with three).
 constexpr int forward_regs(int E) { return E <= 8 ? 64 : E <= 16 ? 80 : 128; }
 constexpr int backward_regs(int E) { return E <= 8 ? 80 : 128; }
 constexpr int kMaxThreads = 512;

@@ -11,21 +11,30 @@
 //     S_0   = w^L S0 + sum_s (w^(s+1) v_s) k_s^T.
 // Only powers w^0 .. w^128 of the head's decay appear, all <= 1, so every w in [0, 1] is exact.
 //
-// One CTA of eight warps walks the chunks of one (b, h) (or of one segment of it), two CTAs per SM (so
-// 128 registers a thread, which the kernel needs without spilling).  Warp w has token rows (TMEM lanes)
-// 32 (w % 4) .. + 31 and half w / 4 of their columns; the warp with the least to do in P also issues the
-// TMA loads and the MMAs.  Per chunk, float32 accumulation:
+// One CTA of eight warps walks the chunks of one (b, h) (or of one segment of it), two CTAs per SM: 106 KB of
+// shared memory and 256 TMEM columns each, and what one waits for overlaps the other's work.  Warp w has
+// token rows (TMEM lanes) 32 (w % 4) .. + 31 and half w / 4 of their columns; the warp with nothing to do
+// in P issues the TMA loads and the MMAs.  Per chunk, float32 accumulation:
 //     MMA1  [128 x 192] = Q [K; S0]^T                K-major tiles, as TMA and the warps left them
 //     MMA2  [128 x 64]  = P V                        P from TMEM in bf16, V as TMA left it (MN-major)
 //     MMA3  [64 x 64]   = V1 K + V2 K + V3 K         V1 + V2 + V3 = w^(L-1-s) v_s, MN-major
 // MMA3 and the new state run beside P and MMA2, and the tiles of the next chunk arrive meanwhile.
 // The state stays in float32 registers across chunks (16 elements per thread).  Roundings to bf16:
 //   P: one per product, as large as the rounding of out itself, and averaged over the tokens;
-//   S0 in MMA1: once, 2^-8 at most like P; it reaches out only.  A second term cost the 8 KB and the 64
-//   TMEM columns that let MMA3 run early (685 us against @@ at B4 T16384 H64);
+//   S0 in MMA1: once, 2^-8 at most like P; it reaches out only (out's error against float64 is 0.0023 of
+//   its norm, 0.0017 of which is out's own rounding).  A second term cost the shared memory and the TMEM
+//   columns that let MMA3 run beside P (B4 T16384 H64: 685 us with it, 625 without);
 //   w^(L-1-s) v_s in MMA3: three terms, 2^-24 at most, because these sums are the state: with two terms
 //   they would be 2.7e-6 off on average, the three leave 4e-7 (float32 sums of products alone: 2e-7).
 // k, q and v enter their products as they are, exactly.
+//
+// Measured on B200: B4 T16384 H64 (2.15 GB) 431 us, 500 to 535 us back to back, where the card's power
+// limit takes the clock from 1.97 to 1.55 GHz; 296 chains (2 per SM) of 8192 tokens 5.4 TB/s, 83 % of
+// measured HBM.  A chunk takes 2.5 us alone on an SM and 3.6 us with another CTA: no unit is full (issue
+// slots 33 %, tensor pipe 40 %, shared memory about half), the chain from barrier to barrier is what is
+// left.  Steps that carried: MMAs under elect.sync (7 cycles to issue against 90), M = 64 for MMA3 (35 cycles
+// an MMA against 50), no spills (L1 is 4 KB here), powers in registers, tiles that change places.  Tried and
+// not kept, no faster: a ninth warp for the issuing, 16 warps per CTA, a second term of S0.
 #include <cuda.h>
 
 #include "linattn.h"
@@ -149,7 +158,8 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
   constexpr int kStore = kRev ? 4 : 3;  // issues the TMA stores of out
   if (warp == kLead) {
     if (elected) {
-      for (int i = 0; i < kBars; ++i) tc::mbar_init(bars + i, i == B_READY || i == B_SPLIT ? 8 : i == B_P ? 7 : i == B_QK && kOut ? 2 : 1);
+      for (int i = 0; i < kBars; ++i)
+        tc::mbar_init(bars + i, i == B_READY || i == B_SPLIT ? 8 : i == B_P ? 7 : i == B_QK && kOut ? 2 : 1);
       tc::fence_mbar_init();
       *bad = 0;
       *stop = 0;
@@ -325,7 +335,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
         load(&maps.v, tile_q, B_V, it + 1);
         ++begun[B_V];
       }
-      // P by column groups of 32: half and half + 2 for a warp, all four for the lead's partner.  P goes over
+      // P by column groups of 32: half and half + 2 for a warp, all four for the partner of kLead.  P goes over
       // products that this warp has read: group g to columns 32 (g % 2) + 16 (g / 2) .. + 15.
       // (The powers come from repeated products: tables in shared memory had to wait for MMA3, which takes
       // nearly all of its bandwidth meanwhile.)
@@ -441,7 +451,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     }
     tc::tc_fence_before();
     if (tid == 0) *stop = *bad;
-    named_sync(5, kThreads);
+    named_sync(1, kThreads);
     if (*stop) break;
     if (kOut && L == kChunk && warp == kStore && elected) {
       tma_store_3d(&maps.out, sm + OFF_V1, 0, h, static_cast<int>(sg.lo) + c * kChunk);

@@ -277,6 +277,29 @@ def test_long_sequence_state_keeps_its_precision():
     assert float((s.double() - want).norm() / want.norm()) <= 2e-6
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_bad_values_stay_in_their_sequence(bad):
+    """One bad value of head 1 of row 1: nothing else changes, and of that sequence only the tokens from its
+    chunk on."""
+    r, k, v, w, dy, st, ds = inputs(2, 400, 3, 24, torch.bfloat16)
+    w = torch.full_like(w, 0.9)
+    clean = lib7.linattn_prefill(r, k, v, w, st) + lib7.linattn_backward(r, k, v, w, dy, st, ds)
+    v[1, 200, 1, 5] = bad
+    got = lib7.linattn_prefill(r, k, v, w, st) + lib7.linattn_backward(r, k, v, w, dy, st, ds)
+    done()
+    for n, (a, b) in enumerate(zip(got, clean)):
+        head = 2 if a.shape == r.shape else 1
+        assert torch.equal(a[0], b[0]), n
+        others = [h for h in range(3) if h != 1]
+        assert torch.equal(a[1].transpose(0, head - 1)[others], b[1].transpose(0, head - 1)[others]), n
+    y, s = got[:2]
+    assert torch.equal(y[1, :128, 1], clean[0][1, :128, 1])
+    assert not bool(torch.isfinite(y[1, 200:, 1, 5]).any()) and not bool(torch.isfinite(s[1, 1, 5]).any())
+    dr, dk = got[2:4]
+    assert torch.equal(dr[1, :128, 1], clean[2][1, :128, 1])  # dr reads the states before it alone
+    assert torch.equal(dk[1, 256:, 1], clean[3][1, 256:, 1])  # dk of a later token does not see an earlier v
+
+
 def test_guard_bands():
     """Nothing outside the outputs is written: outputs inside larger buffers, odd sizes."""
     B, T, H = 2, 333, 3
