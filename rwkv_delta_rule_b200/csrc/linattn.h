@@ -17,6 +17,7 @@ template <typename TIn> struct Pass {
   float *s_out;          // [B, H, 64, 64] or nullptr
   int s_in_t, s_out_t;   // the state is stored transposed there
   float *ws;             // nseg > 1: [B, H, nseg, 64, 64], slot z is the state that segment z begins with
+                         // (joined), or what the segment before it adds to the state
   int reverse;
 };
 // Passes over operands of one shape that run side by side (the backward has three).
@@ -33,21 +34,26 @@ struct Shape {
   long long total_T;
   int H;
   int nseg;     // segments per sequence (1: the whole sequence)
+  int joined;   // nseg > 1: the slots of ws hold the states that segments begin with, not yet what they add
   int seg_len;  // tokens per segment (on the tensor cores whole chunks); the last segment runs to the sequence's end
 };
 
 // Tokens lo .. lo + len - 1 of the packed operands; `first` / `last`: this segment begins / ends the
-// sequence.  len = -1: nothing to do.
+// sequence, which has n segments, the last one of last_len tokens.  len = -1: nothing to do.
 struct Segment {
   long long lo;
   int len;
   bool first, last;
+  int n, last_len;
 };
 __device__ __forceinline__ Segment segment(const Shape &P, int b, int z) {
   const SeqBounds sb = seq_bounds(P.cu_seqlens, b, P.T, P.total_T);
-  Segment s{0, -1, z == 0, false};
+  Segment s{0, -1, z == 0, false, 0, 0};
   if (sb.len < 0) return s;
   const long long off = static_cast<long long>(z) * P.seg_len;
+  const int segs = sb.len <= P.seg_len ? 1 : (sb.len - 1) / P.seg_len + 1;
+  s.n = segs < P.nseg ? segs : P.nseg;
+  s.last_len = sb.len - (s.n - 1) * P.seg_len;  // below 2^31: the segments before are within the sequence
   if (z > 0 && off >= sb.len) return s;
   const long long left = sb.len - off;
   s.lo = sb.start + off;

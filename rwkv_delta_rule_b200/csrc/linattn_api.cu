@@ -51,7 +51,7 @@ lin::Shape shape(const float *w, const int32_t *cu, int B, int T, long long tota
   if (n > room) n = room < 2 ? 1 : static_cast<int>(room);
   const long long u = chunk ? unit(true) : 16, len = ((max_T + n - 1) / n + u - 1) / u * u;
   if (n > 1) n = static_cast<int>((max_T + len - 1) / len);
-  return lin::Shape{w, cu, T, total_T, H, n, n > 1 ? static_cast<int>(len) : 0x7fffff80};
+  return lin::Shape{w, cu, T, total_T, H, n, 1, n > 1 ? static_cast<int>(len) : 0x7fffff80};
 }
 
 template <typename TIn> cudaError_t one_sweep(const lin::Passes<TIn> &p, const lin::Shape &s, int B, bool chunk,
@@ -62,14 +62,26 @@ template <typename TIn> cudaError_t one_sweep(const lin::Passes<TIn> &p, const l
   return launch_linattn_scan(p, s, B, stream);
 }
 
-template <typename TIn> cudaError_t run_passes(const lin::Passes<TIn> &p, const lin::Shape &s, int B, bool chunk,
+// Up to this many segments the tensor-core pass joins their states itself, in place of a launch between
+// (B8 T4096 H12, 3 segments: JOINUS); each CTA then reads the 16 KB of every segment before its own.
+constexpr int kOwnJoin = 8;
+
+template <typename TIn> cudaError_t run_passes(const lin::Passes<TIn> &p, lin::Shape s, int B, bool chunk,
                                                cudaStream_t stream) {
   if (s.nseg > 1) {
     lin::Passes<TIn> states = p;
     states.state_only = 1;
-    cudaError_t e = one_sweep(states, s, B, chunk, stream);
-    if (e == cudaSuccess) e = launch_linattn_join(states, s, B, stream);
+    const cudaError_t e = one_sweep(states, s, B, chunk, stream);
     if (e != cudaSuccess) return e;
+    // a state written in place must have been read by every segment before any of them ends
+    bool in_place = false;
+    for (int i = 0; i < p.n; ++i)
+      for (int j = 0; j < p.n; ++j) in_place = in_place || (p.p[i].s_in != nullptr && p.p[i].s_in == p.p[j].s_out);
+    s.joined = !chunk || s.nseg > kOwnJoin || in_place;
+    if (s.joined) {
+      const cudaError_t f = launch_linattn_join(states, s, B, stream);
+      if (f != cudaSuccess) return f;
+    }
   }
   return one_sweep(p, s, B, chunk, stream);
 }

@@ -197,14 +197,31 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     for (int e = 0; e < 8; ++e) sts32((at_s ^ (16 * (e >> 1))) + 1024 * (e & 1), pack2(S[e]));
   };
   {
-    const float *from = !kOut ? nullptr : P.nseg > 1 ? A.ws + (pair * P.nseg + z) * (kN * kN) : A.s_in;
-    if (kOut && P.nseg == 1 && from != nullptr) from += pair * (kN * kN);
-    const int t = P.nseg == 1 && A.s_in_t;
+    // from where the segments' states are joined already, its slot; else the initial state, and what the
+    // segments on the way here add to it
+    const bool joined = P.nseg > 1 && P.joined;
+    const float *from = !kOut ? nullptr : joined ? A.ws + (pair * P.nseg + z) * (kN * kN) : A.s_in;
+    if (kOut && !joined && from != nullptr) from += pair * (kN * kN);
+    const int t = !joined && A.s_in_t;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       S[e] = from == nullptr ? make2(0.f, 0.f)
                              : make2(from[state_at(t, i0 + 8 * (e & 1), j0 + 8 * (e >> 1))],
                                      from[state_at(t, i0 + 8 * (e & 1), j0 + 8 * (e >> 1) + 1)]);
+    if (kOut && !joined && P.nseg > 1) {
+      const double wd = P.w[h];
+      const float wl = static_cast<float>(powi(wd, P.seg_len));
+      const int steps = kRev ? sg.n - 1 - z : z;
+      for (int s = 1; s <= steps; ++s) {
+        const float *u = A.ws + (pair * P.nseg + (kRev ? sg.n - 1 - s : s)) * (kN * kN);
+        const float f = kRev && s == 1 ? static_cast<float>(powi(wd, sg.last_len)) : wl;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 x = *reinterpret_cast<const float2 *>(u + (i0 + 8 * (e & 1)) * kN + j0 + 8 * (e >> 1));
+          S[e] = fma2(S[e], make2(f, f), make2(x.x, x.y));
+        }
+      }
+    }
     if (kOut) put_state();
   }
   tc::fence_proxy_async_smem();
@@ -309,13 +326,6 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     if (warp == kLead) {
       if ((kOut || wait(B_QK, it)) && wait(B_SPLIT, it) && elected) {
         tc::tc_fence_after();
-        constexpr uint32_t d3 = tc::instr_desc(tc::kFmtBF16, 64, 64, true, true);
-#pragma unroll
-        for (int ks = 0; ks < 24; ++ks)
-          tc::mma_ss(0, tmem + TM_X, tc::smem_desc(sm + OFF_V1 + ks * 2048, kTile, 1024),
-                     tc::smem_desc(sm + tile_k + (ks & 7) * 2048, kTile, 1024), d3, ks > 0);
-        tc::mma_commit(bars + B_M3);
-        ++begun[B_M3];
         if (!kOut && it + 1 < nchunks && !*bad) {
           // every warp is through with V and with its waits for these tiles, and MMA3 of the chunk before with
           // the other K
@@ -324,6 +334,13 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
           ++begun[B_QK];
           ++begun[B_V];
         }
+        constexpr uint32_t d3 = tc::instr_desc(tc::kFmtBF16, 64, 64, true, true);
+#pragma unroll
+        for (int ks = 0; ks < 24; ++ks)
+          tc::mma_ss(0, tmem + TM_X, tc::smem_desc(sm + OFF_V1 + ks * 2048, kTile, 1024),
+                     tc::smem_desc(sm + tile_k + (ks & 7) * 2048, kTile, 1024), d3, ks > 0);
+        tc::mma_commit(bars + B_M3);
+        ++begun[B_M3];
       }
       __syncwarp();
     }

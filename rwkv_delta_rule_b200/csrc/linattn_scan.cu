@@ -21,6 +21,10 @@ template <typename TIn> struct Tile {
   static constexpr size_t kSmem = 2 * kElems * sizeof(TIn) + kTok * kN * sizeof(float);
 };
 
+template <int n> struct Count {
+  static constexpr int value = n;
+};
+
 template <typename TIn, bool kOut>
 __device__ __forceinline__ void stage(const Pass<TIn> &A, TIn *buf, long long tok0, int ntok, int H, int h) {
   using C = Tile<TIn>;
@@ -77,46 +81,68 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
     }
     __syncthreads();
     const TIn *buf = bufs + (i & 1) * C::kElems;
-#pragma unroll 4
-    for (int u = 0; u < ntok; ++u) {
-      const int tt = kRev ? ntok - 1 - u : u;
-      const TIn *tk = buf + tt * 3 * kN;
-      float kk[8], vv[4], p[4];
-      Elem<TIn>::load4(tk + kN + 4 * q, kk);
-      Elem<TIn>::load4(tk + kN + 32 + 4 * q, kk + 4);
-      Elem<TIn>::load4(tk + 2 * kN + row0, vv);
+    // kG tokens at a time: their operands are loaded before, and their row sums meet after the walk through
+    // the state, so that neither's latency is paid per token
+    auto group = [&](int u0, auto count) {
+      constexpr int kG = decltype(count)::value;
+      float kk[kG][8], vv[kG][4], qq[kOut ? kG : 1][8], p[kOut ? kG : 1][4];
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[m][e] = kRev ? fmaf(vv[m], kk[e], s[m][e]) : fmaf(s[m][e], w, vv[m] * kk[e]);
-      if (kOut) {
-        float qq[8];
-        Elem<TIn>::load4(tk + 4 * q, qq);
-        Elem<TIn>::load4(tk + 32 + 4 * q, qq + 4);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          float x = s[m][0] * qq[0], y = s[m][1] * qq[1];
-#pragma unroll
-          for (int e = 2; e < 8; e += 2) {
-            x = fmaf(s[m][e], qq[e], x);
-            y = fmaf(s[m][e + 1], qq[e + 1], y);
-          }
-          p[m] = x + y;
+      for (int j = 0; j < kG; ++j) {
+        const TIn *tk = buf + (kRev ? ntok - 1 - u0 - j : u0 + j) * 3 * kN;
+        Elem<TIn>::load4(tk + kN + 4 * q, kk[j]);
+        Elem<TIn>::load4(tk + kN + 32 + 4 * q, kk[j] + 4);
+        Elem<TIn>::load4(tk + 2 * kN + row0, vv[j]);
+        if (kOut) {
+          Elem<TIn>::load4(tk + 4 * q, qq[j]);
+          Elem<TIn>::load4(tk + 32 + 4 * q, qq[j] + 4);
         }
-        const bool h4 = (q & 4) != 0, h2 = (q & 2) != 0;
-        const float a0 = (h4 ? p[2] : p[0]) + __shfl_xor_sync(0xffffffffu, h4 ? p[0] : p[2], 4);
-        const float a1 = (h4 ? p[3] : p[1]) + __shfl_xor_sync(0xffffffffu, h4 ? p[1] : p[3], 4);
-        float y = (h2 ? a1 : a0) + __shfl_xor_sync(0xffffffffu, h2 ? a0 : a1, 2);
-        y += __shfl_xor_sync(0xffffffffu, y, 1);
-        if ((q & 1) == 0) ys[tt * kN + row0 + (h4 ? 2 : 0) + (h2 ? 1 : 0)] = y;
       }
-      if (kRev) {
+#pragma unroll
+      for (int j = 0; j < kG; ++j) {
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[m][e] *= w;
+          for (int e = 0; e < 8; ++e)
+            s[m][e] = kRev ? fmaf(vv[j][m], kk[j][e], s[m][e]) : fmaf(s[m][e], w, vv[j][m] * kk[j][e]);
+        if (kOut) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            float x = s[m][0] * qq[j][0], y = s[m][1] * qq[j][1];
+#pragma unroll
+            for (int e = 2; e < 8; e += 2) {
+              x = fmaf(s[m][e], qq[j][e], x);
+              y = fmaf(s[m][e + 1], qq[j][e + 1], y);
+            }
+            p[j][m] = x + y;
+          }
+        }
+        if (kRev) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[m][e] *= w;
+        }
       }
-    }
+      if (kOut) {
+        const bool h4 = (q & 4) != 0, h2 = (q & 2) != 0;
+        float y[kG];
+#pragma unroll
+        for (int j = 0; j < kG; ++j) {
+          const float a0 = (h4 ? p[j][2] : p[j][0]) + __shfl_xor_sync(0xffffffffu, h4 ? p[j][0] : p[j][2], 4);
+          const float a1 = (h4 ? p[j][3] : p[j][1]) + __shfl_xor_sync(0xffffffffu, h4 ? p[j][1] : p[j][3], 4);
+          y[j] = (h2 ? a1 : a0) + __shfl_xor_sync(0xffffffffu, h2 ? a0 : a1, 2);
+        }
+#pragma unroll
+        for (int j = 0; j < kG; ++j) {
+          y[j] += __shfl_xor_sync(0xffffffffu, y[j], 1);
+          if ((q & 1) == 0)
+            ys[(kRev ? ntok - 1 - u0 - j : u0 + j) * kN + row0 + (h4 ? 2 : 0) + (h2 ? 1 : 0)] = y[j];
+        }
+      }
+    };
+    int u = 0;
+    for (; u + 4 <= ntok; u += 4) group(u, Count<4>());
+    for (; u < ntok; ++u) group(u, Count<1>());
     __syncthreads();
     if (kOut) {
       for (int e = tid; e < ntok * kN; e += kThreads)
@@ -163,8 +189,8 @@ template <typename TIn> __global__ void __launch_bounds__(256) linattn_join_kern
   pdl_trigger();
   const SeqBounds sb = seq_bounds(P.cu_seqlens, b, P.T, P.total_T);
   if (sb.len < 0) return;
-  const long long segs = (static_cast<long long>(sb.len) + P.seg_len - 1) / P.seg_len;
-  const int n = static_cast<int>(segs < 1 ? 1 : segs < P.nseg ? segs : P.nseg);
+  const Segment sg = segment(P, b, 0);
+  const int n = sg.n;
   const long long pair = static_cast<long long>(b) * P.H + h;
   const int e4 = (blockIdx.z & 3) * 256 + threadIdx.x, row = e4 >> 4, col = 4 * (e4 & 15);
   const double w = P.w[h];
@@ -191,7 +217,7 @@ template <typename TIn> __global__ void __launch_bounds__(256) linattn_join_kern
       if (i0 + j < n) {
         // the decay over the segment before; the sequence's last one may be of another length
         float f = wl;
-        if (A.reverse && i0 + j == 1) f = static_cast<float>(powi(w, sb.len - static_cast<long long>(n - 1) * P.seg_len));
+        if (A.reverse && i0 + j == 1) f = static_cast<float>(powi(w, sg.last_len));
         s = make_float4(fmaf(s.x, f, u[j].x), fmaf(s.y, f, u[j].y), fmaf(s.z, f, u[j].z), fmaf(s.w, f, u[j].w));
         *slot(i0 + j) = s;
       }
