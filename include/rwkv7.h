@@ -393,8 +393,8 @@ RWKV7_API rwkv7_status rwkv7_wkv_backward_bf16(int B, int T, int H, int N, const
  *   operands alone, no checkpoints: with G_t = dL/dS_t = dy_t r_t^T + w G_{t+1},
  *     dr_t = S_t^T dy_t,  dk_t = G_t^T v_t,  dv_t = G_t k_t,  ds_in = w G_0.
  *   dr, dk, dv [B,T,H,64] are bfloat16 like the operands (each is written once, nothing is
- *   accumulated in them); ds_in float32 or NULL, and may equal ds_out.  No other output may overlap an
- *   input.  w gets no gradient. */
+ *   accumulated in them); ds_in float32 or NULL, and may equal ds_out or s_in.  No other output may overlap
+ *   an input.  w gets no gradient. */
 RWKV7_API long long rwkv7_linattn_workspace(int B, int max_T, int H);
 RWKV7_API long long rwkv7_linattn_backward_workspace(int B, int T, int H);
 

@@ -475,21 +475,22 @@ template <typename T> __global__ void __launch_bounds__(1024) layer_norm_backwar
   }
 }
 
-// The column sums of long vectors: one thread per column, rows mb, mb + mblocks, ...; blockIdx = (mb, column tile).
+// The column sums of long vectors: one thread per column, rows mb, mb + mblocks, ...; blockIdx = (column tile, mb):
+// there may be 65536 tiles, one more than a grid has in y.
 template <typename T> __global__ void __launch_bounds__(256) layer_norm_columns_kernel(const Args<T> A) {
   pdl_wait();
   pdl_trigger();
-  const long long GD = static_cast<long long>(A.G) * A.D, c = static_cast<long long>(blockIdx.y) * 256 + threadIdx.x;
+  const long long GD = static_cast<long long>(A.G) * A.D, c = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (c >= GD) return;
   const int g = static_cast<int>(c / A.D);
   float aw = 0.f, ab = 0.f;
-  for (long long m = blockIdx.x; m < A.M; m += gridDim.x) {
+  for (long long m = blockIdx.y; m < A.M; m += gridDim.y) {
     const float d = Elem<T>::load(A.dy + m * GD + c);
     aw = fmaf(d, (Elem<T>::load(A.x + m * GD + c) - A.mean[m * A.G + g]) * A.rstd[m * A.G + g], aw);
     ab += d;
   }
-  A.partial[blockIdx.x * 2 * GD + c] = aw;
-  A.partial[(blockIdx.x * 2 + 1) * GD + c] = ab;
+  A.partial[blockIdx.y * 2 * GD + c] = aw;
+  A.partial[(blockIdx.y * 2 + 1) * GD + c] = ab;
 }
 
 // dw and db from the partial sums [n][2][GD]: 8 columns and 128 slices of n per CTA.
@@ -670,7 +671,7 @@ cudaError_t launch_layer_norm_backward(const TIn *dy, const TIn *x, const float 
     if (P.loop) {
       e = launch(layer_norm_backward_long_kernel<TIn>, dim3(static_cast<unsigned>(M) * G), 1024, 0, stream, A);
       if (e == cudaSuccess && dw != nullptr)
-        e = launch(layer_norm_columns_kernel<TIn>, dim3(P.mblocks, ceil_div(GD, 256)), 256, 0, stream, A);
+        e = launch(layer_norm_columns_kernel<TIn>, dim3(ceil_div(GD, 256), P.mblocks), 256, 0, stream, A);
     } else {
       e = launch_any(P, A, true, stream);
     }

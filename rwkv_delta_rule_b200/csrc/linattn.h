@@ -99,8 +99,7 @@ cudaError_t launch_waiting(void (*kernel)(KArgs...), dim3 grid, unsigned block, 
 
 // The batch row of a CTA: rows of a ragged batch are taken from the longest to the shortest (up to kMaxSorted
 // rows; equal ones in order), so that none is left to the end: 16 rows of up to 2500 tokens, H32, 95 us against
-// 112 in their own order.  `lens`, kMaxSorted ints of shared memory and
-// one more.  Called by a whole CTA of at least kMaxSorted / 2 threads.
+// 112 in their own order.  `lens`: kMaxSorted + 1 ints of shared memory.  Called by a whole CTA.
 constexpr int kMaxSorted = 256;
 __device__ __forceinline__ int sorted_row(const Shape &P, int b, int B, int *lens) {
   if (P.cu_seqlens == nullptr || B > kMaxSorted) return b;

@@ -179,6 +179,15 @@ def test_guard_bands():
         check(x, dy, w, b, 1e-5, y, mean, rstd, dx, dw, db)
 
 
+def test_most_columns():
+    """G * D of 2^24, the most there may be: 65536 tiles of columns."""
+    x, dy, w, b = inputs(2, 256, 65536, torch.bfloat16, 9)
+    y, mean, rstd = lib7.layer_norm(x, w, b)
+    dx, dw, db = lib7.layer_norm_backward(dy, x, w, mean, rstd)
+    torch.cuda.synchronize()
+    check(x, dy, w, b, 1e-5, y, mean, rstd, dx, dw, db)
+
+
 def test_rows_past_32_bits():
     """More than 2^31 elements: the last rows are right."""
     M, D = (1 << 31) // 4096 + 9, 4096

@@ -197,6 +197,23 @@ def test_backward_with_less_workspace_and_in_place(states):
     ref.check_mix(dv, io, k, r, dy, w, ds, reverse=True, what="dv")
 
 
+@pytest.mark.parametrize("T", [20, 1000])
+@pytest.mark.parametrize("states", [0, 3])
+def test_backward_over_the_initial_state(states, T):
+    """ds_in may be s_in, which another pass reads."""
+    B, H = 40, 7
+    r, k, v, w, dy, st, ds = inputs(B, T, H, 16, torch.bfloat16)
+    dr, dk, dv = (torch.full_like(r, float("nan")) for _ in range(3))
+    io = st.clone()
+    ws = torch.full((3 * states * B * H * 4096,), float("nan"), device="cuda") if states else None
+    lib7.rwkv7_linattn_backward_bf16(r, k, v, w, io, dy, ds, dr, dk, dv, io, ws)
+    done()
+    t = lambda x: x.transpose(-1, -2)  # noqa: E731
+    ref.check_mix(dr, None, dy, v, k, w, t(st), what="dr")
+    ref.check_mix(dk, None, v, dy, r, w, t(ds), reverse=True, what="dk")
+    ref.check_mix(dv, io, k, r, dy, w, ds, reverse=True, what="dv")
+
+
 def test_backward_without_state_gradient():
     r, k, v, w, dy, st, ds = inputs(1, 200, 2, 15, torch.bfloat16)
     want = lib7.linattn_backward(r, k, v, w, dy, st, ds)
