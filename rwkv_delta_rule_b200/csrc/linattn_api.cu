@@ -17,18 +17,18 @@ rwkv7_status from_cuda(cudaError_t e) { return e == cudaSuccess ? RWKV7_OK : RWK
 constexpr long long kStateBytes = kN * kN * sizeof(float);
 
 // bf16 passes run on the tensor cores from this length on.  Measured on B200 (token by token / tensor cores,
-// us): B1 H12 T16 6.2 / 6.4, T32 9.1 / 6.6; B8 H12 T24 7.8 / 6.8, T32 9.3 / 6.8; B64 H32 T32 56 / 58, T48 79 / 58;
-// B256 H16 T24 169 / 172, T32 188 / 172.
+// us): B1 H12 T16 4.8 / 6.1, T32 9.1 / 6.1; B8 H12 T32 9.3 / 6.4; B64 H32 T32 48 / 52, T40 59 / 52; B256 H16
+// T32 93 / 102, T40 114 / 102.
 constexpr long long kChunkMinT = 32;
 template <typename TIn> bool use_chunk(long long max_T) { return sizeof(TIn) == 2 && max_T >= kChunkMinT; }
 
 // Segments a sequence of at most T tokens is split into, for `chains` sequences that run side by side: as
-// many as fill the CTAs that the device runs at once (2 per SM on the tensor cores, 4 of the
-// token-by-token kernel), of at least one chunk, or of 32 tokens (token by token, B1 T1000 H12 float32:
-// 90 us with segments of 256 tokens, 42 with 64, 37 with 32).
-int unit(bool chunk) { return chunk ? 128 : 32; }
+// many as fill the CTAs that the device runs at once (2 per SM on the tensor cores, 7 of the token-by-token
+// kernel; float32 B4 T1000 H12 87 us with 4, 62 with 7), of whole chunks, or of 24 tokens, 48 tokens staying
+// whole (float32 B1 H12: T1000 45 us in segments of 96 tokens, 33 of 32; T64 13.3 whole, 12.5 in three;
+// bf16 T32 9.1 whole, 9.7 in two).  Lengths are multiples of 8 tokens, of 128 on the tensor cores.
 int segments(long long chains, long long T, bool chunk) {
-  const long long want = (chunk ? 296 : 592) / chains, most = T / unit(chunk);
+  const long long want = (chunk ? 296 : 1036) / chains, most = chunk ? T / 128 : T <= 48 ? 1 : (T + 23) / 24;
   const long long n = want < most ? want : most;
   return n < 1 ? 1 : static_cast<int>(n);
 }
@@ -49,7 +49,7 @@ lin::Shape shape(const float *w, const int32_t *cu, int B, int T, long long tota
   int n = segments(passes * pairs, max_T, chunk);
   const long long room = bytes / (passes * pairs * kStateBytes);
   if (n > room) n = room < 2 ? 1 : static_cast<int>(room);
-  const long long u = chunk ? unit(true) : 16, len = ((max_T + n - 1) / n + u - 1) / u * u;
+  const long long u = chunk ? 128 : 8, len = ((max_T + n - 1) / n + u - 1) / u * u;
   if (n > 1) n = static_cast<int>((max_T + len - 1) / len);
   return lin::Shape{w, cu, T, total_T, H, n, 1, n > 1 ? static_cast<int>(len) : 0x7fffff80};
 }

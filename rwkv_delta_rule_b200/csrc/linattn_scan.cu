@@ -2,20 +2,21 @@
 // in registers:  S <- w S + v k^T,  y = S q,  and the same walked from the last token for gradients.
 //
 // One CTA of 128 threads holds a (b, h) pair's 64 x 64 state: thread (rs, q) has rows 4 rs .. 4 rs + 3
-// and columns 4 q .. 4 q + 3, 32 + 4 q .. 32 + 4 q + 3.  The chain through the state is one
-// multiply-add per token, so the walk is bound by its 96 float32 operations and 5 shared-memory loads
-// per thread and token, not by latency.  The read-out's row sums meet in a 4-shuffle reduce-scatter
-// over the 8 lanes of a row group.  Operands are staged by cp.async in double-buffered tiles.
-// Measured on B200: float32 B1 T1000 H12 37 us (states, join and outputs: 11, 5 and 17 us in launches of 20
-// segments of 48 tokens); bf16 B8 T4096 H12 515 us, which the tensor cores do in 78.
+// and columns 4 q .. 4 q + 3, 32 + 4 q .. 32 + 4 q + 3, in pairs (packed operations are the scalar ones, two at a
+// time).  The chain through the state is one multiply-add per token, so the walk is bound by its 48 packed
+// operations, 5 shared-memory loads and the row sums per thread and token.  These sums meet in a 4-shuffle
+// reduce-scatter over the 8 lanes of a row group.  Operands are staged by cp.async in double-buffered tiles.
+// Measured on B200: float32 B1 T1000 H12 30 us (states, join and outputs in three launches, 42
+// segments of 24 tokens); B8 T4096 H12 454, where tiles twice as long and 4 CTAs per SM took 558 and scalar operations 603.
 #include "linattn.h"
+#include "packed.cuh"
 
 namespace rwkv7 {
 namespace lin {
 
 constexpr int kThreads = 128;
 template <typename TIn> struct Tile {
-  static constexpr int kTok = sizeof(TIn) == 2 ? 32 : 16;     // tokens per tile
+  static constexpr int kTok = sizeof(TIn) == 2 ? 16 : 8;     // tokens per tile
   static constexpr int kEPC = 16 / static_cast<int>(sizeof(TIn));
   static constexpr int kElems = kTok * 3 * kN;                // q, k, v
   static constexpr size_t kSmem = 2 * kElems * sizeof(TIn) + kTok * kN * sizeof(float);
@@ -24,6 +25,13 @@ template <typename TIn> struct Tile {
 template <int n> struct Count {
   static constexpr int value = n;
 };
+
+template <typename TIn> __device__ __forceinline__ void load_pairs(const TIn *p, f32x2 *x) {
+  float f[4];
+  Elem<TIn>::load4(p, f);
+  x[0] = make2(f[0], f[1]);
+  x[1] = make2(f[2], f[3]);
+}
 
 template <typename TIn, bool kOut>
 __device__ __forceinline__ void stage(const Pass<TIn> &A, TIn *buf, long long tok0, int ntok, int H, int h) {
@@ -48,18 +56,19 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
   if (!kOut && (kRev ? sg.first : sg.last)) return;
   const long long pair = static_cast<long long>(b) * P.H + h;
   const int tid = threadIdx.x, q = tid & 7, row0 = 4 * (tid >> 3);
-  const float w = P.w[h];
+  const f32x2 w2 = make2(P.w[h], P.w[h]);
 
-  float s[4][8];
+  f32x2 s[4][4];  // columns in pairs
   const float *from = !kOut ? nullptr : P.nseg > 1 ? A.ws + (pair * P.nseg + z) * (kN * kN) : A.s_in + pair * (kN * kN);
   const int from_t = P.nseg == 1 && A.s_in_t;
   if (P.nseg == 1 && A.s_in == nullptr) from = nullptr;
 #pragma unroll
   for (int m = 0; m < 4; ++m)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int col = (e >> 2) * 32 + 4 * q + (e & 3);
-      s[m][e] = from == nullptr ? 0.f : from[state_at(from_t, row0 + m, col)];
+    for (int e = 0; e < 4; ++e) {
+      const int col = (e >> 1) * 32 + 4 * q + 2 * (e & 1);
+      s[m][e] = from == nullptr ? make2(0.f, 0.f)
+                                : make2(from[state_at(from_t, row0 + m, col)], from[state_at(from_t, row0 + m, col + 1)]);
     }
 
   const int ntiles = (sg.len + C::kTok - 1) / C::kTok;
@@ -85,16 +94,20 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
     // the state, so that neither's latency is paid per token
     auto group = [&](int u0, auto count) {
       constexpr int kG = decltype(count)::value;
-      float kk[kG][8], vv[kG][4], qq[kOut ? kG : 1][8], p[kOut ? kG : 1][4];
+      f32x2 kk[kG][4], vv[kG][4], qq[kOut ? kG : 1][4];
+      float p[kOut ? kG : 1][4];
 #pragma unroll
       for (int j = 0; j < kG; ++j) {
         const TIn *tk = buf + (kRev ? ntok - 1 - u0 - j : u0 + j) * 3 * kN;
-        Elem<TIn>::load4(tk + kN + 4 * q, kk[j]);
-        Elem<TIn>::load4(tk + kN + 32 + 4 * q, kk[j] + 4);
-        Elem<TIn>::load4(tk + 2 * kN + row0, vv[j]);
+        load_pairs(tk + kN + 4 * q, kk[j]);
+        load_pairs(tk + kN + 32 + 4 * q, kk[j] + 2);
+        float v[4];
+        Elem<TIn>::load4(tk + 2 * kN + row0, v);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) vv[j][m] = make2(v[m], v[m]);
         if (kOut) {
-          Elem<TIn>::load4(tk + 4 * q, qq[j]);
-          Elem<TIn>::load4(tk + 32 + 4 * q, qq[j] + 4);
+          load_pairs(tk + 4 * q, qq[j]);
+          load_pairs(tk + 32 + 4 * q, qq[j] + 2);
         }
       }
 #pragma unroll
@@ -102,17 +115,16 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            s[m][e] = kRev ? fmaf(vv[j][m], kk[j][e], s[m][e]) : fmaf(s[m][e], w, vv[j][m] * kk[j][e]);
+          for (int e = 0; e < 4; ++e)
+            s[m][e] = kRev ? fma2(vv[j][m], kk[j][e], s[m][e]) : fma2(s[m][e], w2, mul2(vv[j][m], kk[j][e]));
         if (kOut) {
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            float x = s[m][0] * qq[j][0], y = s[m][1] * qq[j][1];
+            f32x2 t = mul2(s[m][0], qq[j][0]);
 #pragma unroll
-            for (int e = 2; e < 8; e += 2) {
-              x = fmaf(s[m][e], qq[j][e], x);
-              y = fmaf(s[m][e + 1], qq[j][e + 1], y);
-            }
+            for (int e = 1; e < 4; ++e) t = fma2(s[m][e], qq[j][e], t);
+            float x, y;
+            split2(t, x, y);
             p[j][m] = x + y;
           }
         }
@@ -120,7 +132,7 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
 #pragma unroll
           for (int m = 0; m < 4; ++m)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[m][e] *= w;
+            for (int e = 0; e < 4; ++e) s[m][e] = mul2(s[m][e], w2);
         }
       }
       if (kOut) {
@@ -157,9 +169,9 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int col = (e >> 2) * 32 + 4 * q + (e & 3);
-        to[state_at(kOut && A.s_out_t, row0 + m, col)] = s[m][e];
+      for (int e = 0; e < 4; ++e) {
+        const int col = (e >> 1) * 32 + 4 * q + 2 * (e & 1), t = kOut && A.s_out_t;
+        split2(s[m][e], to[state_at(t, row0 + m, col)], to[state_at(t, row0 + m, col + 1)]);
       }
   }
 }
@@ -167,7 +179,7 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
 // blockIdx = (head, batch row, pass and segment); the passes for the states alone leave out the segment
 // that none continues from.
 template <typename TIn, bool kOut>
-__global__ void __launch_bounds__(kThreads) linattn_scan_kernel(const __grid_constant__ Passes<TIn> A, const Shape P) {
+__global__ void __launch_bounds__(kThreads, 7) linattn_scan_kernel(const __grid_constant__ Passes<TIn> A, const Shape P) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ int lens[kMaxSorted + 1];
   pdl_wait();
