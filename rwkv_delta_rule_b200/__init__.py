@@ -412,7 +412,7 @@ def rwkv7_wkv_backward_bf16(r, w, k, v, a, b, states, dy, ds_out, dr, dw, dk, dv
 
 def _fits(t, name: str, dtype, shape, device) -> int:
     """The address of ``t``, which has to be a contiguous tensor of this type and shape on ``device``."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device.index or not t.is_contiguous():
         _check(t, name, dtype, shape)
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}: one device is wanted")
     return t.data_ptr()
@@ -714,13 +714,18 @@ def backward(r, w, k, v, a, b, states, dy, ds_out=None, *, stream=None):
 
 def linattn_prefill(r, k, v, w, s_in=None, *, stream=None):
     """Allocate ``y`` and ``s_out`` and run the linear-attention prefill; returns ``(y, s_out)``."""
-    B, T, H, N = r.shape
-    with _on(stream, r.device):
+    dev, f32, f32_r = _device_of(r, "r"), torch.float32, r.dtype is torch.float32
+    dtype = f32 if f32_r else torch.bfloat16
+    B, T, H, N = shape = _dims(r, "r", "B, T, H, 64")
+    args = (_fits(r, "r", dtype, shape, dev), _fits(k, "k", dtype, shape, dev), _fits(v, "v", dtype, shape, dev),
+            _fits(w, "w", f32, (H,), dev), _fits_or_none(s_in, "s_in", f32, (B, H, N, N), dev))
+    n = load_library().rwkv7_linattn_workspace(B, T, H)
+    with _on(stream, dev):
         y = torch.empty_like(r)
-        s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
-        ws = _workspace(rwkv7_linattn_workspace(B, T, H), r.device)
-    f = rwkv7_linattn_prefill if r.dtype == torch.float32 else rwkv7_linattn_prefill_bf16
-    f(r, k, v, w, s_in, y, s_out, ws, stream)
+        s_out = w.new_empty((B, H, N, N))
+        ws = w.new_empty(n // 4) if n > 0 else None
+    _call_on(dev, stream, "rwkv7_linattn_prefill" if f32_r else "rwkv7_linattn_prefill_bf16", B, T, H, N, *args,
+             y.data_ptr(), s_out.data_ptr(), None if ws is None else ws.data_ptr(), n)
     return y, s_out
 
 
@@ -742,19 +747,26 @@ def linattn_decode_(r, k, v, w, state, y=None, *, stream=None):
     if y is None:
         with _on(stream, r.device):
             y = torch.empty_like(r)
-    f = rwkv7_linattn_decode if r.dtype == torch.float32 else rwkv7_linattn_decode_bf16
+    f = rwkv7_linattn_decode if r.dtype is torch.float32 else rwkv7_linattn_decode_bf16
     f(r, k, v, w, state, y, stream)
     return y
 
 
 def linattn_backward(r, k, v, w, dy, s_in=None, ds_out=None, *, stream=None):
     """Allocate and run the linear-attention backward; returns ``(dr, dk, dv, ds_in)`` (bf16, ds_in float32)."""
-    B, T, H, N = r.shape
-    with _on(stream, r.device):
-        dr, dk, dv = (torch.empty_like(r) for _ in range(3))
-        ds_in = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
-        ws = _workspace(rwkv7_linattn_backward_workspace(B, T, H), r.device)
-    rwkv7_linattn_backward_bf16(r, k, v, w, s_in, dy, ds_out, dr, dk, dv, ds_in, ws, stream)
+    dev, f32, bf16 = _device_of(r, "r"), torch.float32, torch.bfloat16
+    B, T, H, N = shape = _dims(r, "r", "B, T, H, 64")
+    states = (B, H, N, N)
+    args = (_fits(r, "r", bf16, shape, dev), _fits(k, "k", bf16, shape, dev), _fits(v, "v", bf16, shape, dev),
+            _fits(w, "w", f32, (H,), dev), _fits_or_none(s_in, "s_in", f32, states, dev),
+            _fits(dy, "dy", bf16, shape, dev), _fits_or_none(ds_out, "ds_out", f32, states, dev))
+    n = load_library().rwkv7_linattn_backward_workspace(B, T, H)
+    with _on(stream, dev):
+        dr, dk, dv = torch.empty_like(r), torch.empty_like(r), torch.empty_like(r)
+        ds_in = w.new_empty(states)
+        ws = w.new_empty(n // 4) if n > 0 else None
+    _call_on(dev, stream, "rwkv7_linattn_backward_bf16", B, T, H, N, *args, dr.data_ptr(), dk.data_ptr(),
+             dv.data_ptr(), ds_in.data_ptr(), None if ws is None else ws.data_ptr(), n)
     return dr, dk, dv, ds_in
 
 
