@@ -6,8 +6,8 @@
 // time).  The chain through the state is one multiply-add per token, so the walk is bound by its 48 packed
 // operations, 5 shared-memory loads and the row sums per thread and token.  These sums meet in a 4-shuffle
 // reduce-scatter over the 8 lanes of a row group.  Operands are staged by cp.async in double-buffered tiles.
-// Measured on B200: float32 B1 T1000 H12 30 us (states, join and outputs in three launches, 42
-// segments of 24 tokens); B8 T4096 H12 454, where tiles twice as long and 4 CTAs per SM took 558 and scalar operations 603.
+// Measured on B200: float32 B1 T1000 H12 29 us (states, join and outputs in three launches, 42
+// segments of 24 tokens); B8 T4096 H12 435, where tiles twice as long and 4 CTAs per SM took 558 and scalar operations 603.
 #include "linattn.h"
 #include "packed.cuh"
 
@@ -56,7 +56,8 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
   if (!kOut && (kRev ? sg.first : sg.last)) return;
   const long long pair = static_cast<long long>(b) * P.H + h;
   const int tid = threadIdx.x, q = tid & 7, row0 = 4 * (tid >> 3);
-  const f32x2 w2 = make2(P.w[h], P.w[h]);
+  const float w = P.w[h], wp[5] = {1.f, w, w * w, w * w * w, (w * w) * (w * w)};  // powers, for 4 tokens at once
+  const f32x2 w2 = make2(w, w);
 
   f32x2 s[4][4];  // columns in pairs
   const float *from = !kOut ? nullptr : P.nseg > 1 ? A.ws + (pair * P.nseg + z) * (kN * kN) : A.s_in + pair * (kN * kN);
@@ -104,11 +105,27 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
         float v[4];
         Elem<TIn>::load4(tk + 2 * kN + row0, v);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) vv[j][m] = make2(v[m], v[m]);
+        for (int m = 0; m < 4; ++m) {
+          // states alone: all that decays by the group's end is scaled here
+          if (!kOut) v[m] *= wp[kRev ? kG - j : kG - 1 - j];
+          vv[j][m] = make2(v[m], v[m]);
+        }
         if (kOut) {
           load_pairs(tk + 4 * q, qq[j]);
           load_pairs(tk + 32 + 4 * q, qq[j] + 2);
         }
+      }
+      if (!kOut) {
+        const f32x2 f = make2(wp[kG], wp[kG]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[m][e] = mul2(s[m][e], f);
+#pragma unroll
+            for (int j = 0; j < kG; ++j) s[m][e] = fma2(vv[j][m], kk[j][e], s[m][e]);
+          }
+        return;
       }
 #pragma unroll
       for (int j = 0; j < kG; ++j) {
