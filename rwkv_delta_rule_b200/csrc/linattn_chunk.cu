@@ -17,7 +17,7 @@
 // in P issues the TMA loads and the MMAs.  Per chunk, float32 accumulation:
 //     MMA1  [128 x 192] = Q [K; S0]^T                K-major tiles, as TMA and the warps left them
 //     MMA2  [128 x 64]  = P V                        P from TMEM in bf16, V as TMA left it (MN-major)
-//     MMA3  [64 x 64]   = V1 K + V2 K + V3 K         V1 + V2 + V3 = w^(L-1-s) v_s, MN-major
+//     MMA3  [64 x 64]   = V1 K + V2 K (+ V3 K)       V1 + V2 (+ V3) = w^(L-1-s) v_s, MN-major
 // MMA3 and the new state run beside P and MMA2, and the tiles of the next chunk arrive meanwhile.
 // The state stays in float32 registers across chunks (16 elements per thread).  Roundings to bf16:
 //   P: one per product, as large as the rounding of out itself, and averaged over the tokens;
@@ -26,6 +26,8 @@
 //   columns that let MMA3 run beside P (B4 T16384 H64: 685 us with it, 625 without);
 //   w^(L-1-s) v_s in MMA3: three terms, 2^-24 at most, because these sums are the state: with two terms
 //   they would be 2.7e-6 off on average, the three leave 4e-7 (float32 sums of products alone: 2e-7).
+//   Where no state leaves the pass (dr and dk) two, 2^-16 at most: the outputs are bf16, and S0's 2^-8 is
+//   larger (backward B8 T1024 H12 39 us with three there, 34 with two; B2 T4001 H64 220 and 190).
 // k, q and v enter their products as they are, exactly.
 //
 // Measured on B200: B4 T16384 H64 (2.15 GB) 431 us, 500 to 535 us back to back, where the card's power
@@ -191,6 +193,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
   // i0 + 8 u, columns j0 + 8 n, + 1
   const int i0 = 16 * rb + (lane >> 2), j0 = 32 * half + 2 * (lane & 3);
   const uint32_t at_s = sm + OFF_S + i0 * 128u + 4 * (lane & 3) + (((4 * half) ^ (lane >> 2)) << 4);
+  const int terms = kOut && A.s_out == nullptr ? 2 : 3;  // of w^(L-1-s) v_s in MMA3, the second of two rounded
   f32x2 S[8];
   auto put_state = [&]() {  // S in bf16, rows of MMA1's B operand
 #pragma unroll
@@ -284,7 +287,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
       }
     }
 
-    // V1, V2 and V3: this thread's half of its token row, scaled and cut into 8-bit pieces
+    // V1, V2 (and V3): this thread's half of its token row, scaled and cut into 8-bit pieces
     wait(B_V, it);
     if (row >= L) {
 #pragma unroll
@@ -310,13 +313,13 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
           const f32x2 v = mul2(unpack2(in[e]), f);
           p1[e] = high_halves(v);
           const f32x2 r = sub2(v, cut2(v));
-          p2[e] = high_halves(r);
+          p2[e] = terms == 2 ? pack2(r) : high_halves(r);
           p3[e] = high_halves(sub2(r, cut2(r)));
         }
         if (x < 48) lds128((at ^ (x + 16)) + tile_v, in);
         sts128((at ^ x) + OFF_V1, p1);
         sts128((at ^ x) + OFF_V2, p2);
-        sts128((at ^ x) + OFF_V3, p3);
+        if (terms == 3) sts128((at ^ x) + OFF_V3, p3);
       }
     }
     tc::fence_proxy_async_smem();
@@ -335,10 +338,11 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
           ++begun[B_V];
         }
         constexpr uint32_t d3 = tc::instr_desc(tc::kFmtBF16, 64, 64, true, true);
+        for (int t = 0; t < terms; ++t)
 #pragma unroll
-        for (int ks = 0; ks < 24; ++ks)
-          tc::mma_ss(0, tmem + TM_X, tc::smem_desc(sm + OFF_V1 + ks * 2048, kTile, 1024),
-                     tc::smem_desc(sm + tile_k + (ks & 7) * 2048, kTile, 1024), d3, ks > 0);
+          for (int ks = 0; ks < 8; ++ks)
+            tc::mma_ss(0, tmem + TM_X, tc::smem_desc(sm + OFF_V1 + t * kTile + ks * 2048, kTile, 1024),
+                       tc::smem_desc(sm + tile_k + ks * 2048, kTile, 1024), d3, t + ks > 0);
         tc::mma_commit(bars + B_M3);
         ++begun[B_M3];
       }

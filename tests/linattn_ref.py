@@ -72,6 +72,10 @@ def check_mix(out, s_end, q, k, v, w, s0=None, reverse=False, what=""):
             # begins with: each moves its term by at most half a step, and nothing else is in bf16
             tol = tol + BF16_HALF_STEP * (ref.abs() + products(q, k, v, w, reverse)
                                           + state_products(q, k, v, w, s0, reverse)) * (1 + 2.0 ** -6)
+            if s_end is None:
+                # no state leaves the pass, which may then form its products v k^T from two bf16 terms of v: the
+                # first, cut to 8 bits, leaves less than 2^-7 of v, and rounding that to 8 bits leaves 2^-9 of it
+                tol = tol + 2.0 ** -16 * mag
         bad = ~((out.double() - ref).abs() <= tol + 1e-37)
         assert not bool(bad.any()), (what, "out", bad.nonzero()[:4].tolist(), float((out.double() - ref).abs().max()))
     if s_end is not None:
