@@ -6,8 +6,9 @@
 // time).  The chain through the state is one multiply-add per token, so the walk is bound by its 48 packed
 // operations, 5 shared-memory loads and the row sums per thread and token.  These sums meet in a 4-shuffle
 // reduce-scatter over the 8 lanes of a row group.  Operands are staged by cp.async in double-buffered tiles.
-// Measured on B200: float32 B1 T1000 H12 29 us (states, join and outputs in three launches, 42
-// segments of 24 tokens); B8 T4096 H12 435, where tiles twice as long and 4 CTAs per SM took 558 and scalar operations 603.
+// Measured on B200: float32 B1 T1000 H12 28 us (states, join and outputs in three launches, 42
+// segments of 24 tokens); B8 T4096 H12 422, where tiles twice as long with 4 CTAs per SM took 558, with scalar
+// operations 603.
 #include "linattn.h"
 #include "packed.cuh"
 
@@ -96,7 +97,6 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
     auto group = [&](int u0, auto count) {
       constexpr int kG = decltype(count)::value;
       f32x2 kk[kG][4], vv[kG][4], qq[kOut ? kG : 1][4];
-      float p[kOut ? kG : 1][4];
 #pragma unroll
       for (int j = 0; j < kG; ++j) {
         const TIn *tk = buf + (kRev ? ntok - 1 - u0 - j : u0 + j) * 3 * kN;
@@ -115,7 +115,7 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
           load_pairs(tk + 32 + 4 * q, qq[j] + 2);
         }
       }
-      if (!kOut) {
+      if constexpr (!kOut) {
         const f32x2 f = make2(wp[kG], wp[kG]);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
@@ -125,16 +125,15 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
 #pragma unroll
             for (int j = 0; j < kG; ++j) s[m][e] = fma2(vv[j][m], kk[j][e], s[m][e]);
           }
-        return;
-      }
+      } else {
+        float p[kG][4];
 #pragma unroll
-      for (int j = 0; j < kG; ++j) {
+        for (int j = 0; j < kG; ++j) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+          for (int m = 0; m < 4; ++m)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            s[m][e] = kRev ? fma2(vv[j][m], kk[j][e], s[m][e]) : fma2(s[m][e], w2, mul2(vv[j][m], kk[j][e]));
-        if (kOut) {
+            for (int e = 0; e < 4; ++e)
+              s[m][e] = kRev ? fma2(vv[j][m], kk[j][e], s[m][e]) : fma2(s[m][e], w2, mul2(vv[j][m], kk[j][e]));
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             f32x2 t = mul2(s[m][0], qq[j][0]);
@@ -144,15 +143,13 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
             split2(t, x, y);
             p[j][m] = x + y;
           }
-        }
-        if (kRev) {
+          if (kRev) {
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
+            for (int m = 0; m < 4; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[m][e] = mul2(s[m][e], w2);
+              for (int e = 0; e < 4; ++e) s[m][e] = mul2(s[m][e], w2);
+          }
         }
-      }
-      if (kOut) {
         const bool h4 = (q & 4) != 0, h2 = (q & 2) != 0;
         float y[kG];
 #pragma unroll
@@ -174,8 +171,14 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
     for (; u < ntok; ++u) group(u, Count<1>());
     __syncthreads();
     if (kOut) {
-      for (int e = tid; e < ntok * kN; e += kThreads)
-        Elem<TIn>::store(A.out + ((sg.lo + t0 + (e >> 6)) * P.H + h) * kN + (e & 63), ys[e]);
+      for (int e = 4 * tid; e < ntok * kN; e += 4 * kThreads) {
+        const float4 f = *reinterpret_cast<const float4 *>(ys + e);
+        TIn *out = A.out + ((sg.lo + t0 + (e >> 6)) * P.H + h) * kN + (e & 63);
+        if constexpr (sizeof(TIn) == 4)
+          *reinterpret_cast<float4 *>(out) = f;
+        else
+          *reinterpret_cast<uint2 *>(out) = make_uint2(pack2(make2(f.x, f.y)), pack2(make2(f.z, f.w)));
+      }
       // the next tile writes ys only behind the barrier after its loads
     }
   }
