@@ -388,11 +388,14 @@ __global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(backwa
   // this CTA's sums: over its units of each group, in order
   const long long GD = static_cast<long long>(A.G) * A.D;
   float *part = A.partial + (blockIdx.x / A.gblocks) * 2 * GD;
+  // units that the groups leave over (G = 12 groups on 16 units) stand in a slot past the last: their p.g is that of a
+  // unit with rows, and they store nothing
+  const int slot = p.unit / A.gper;
   if (kBlock || A.slots == 1) {
     constexpr int kF = V % 4 == 0 ? 4 : 1;
 #pragma unroll
     for (int n = 0; n < NV; ++n)
-      if (p.g < A.G && n * stride < left) {
+      if (slot < A.slots && p.g < A.G && n * stride < left) {
 #pragma unroll
         for (int e = 0; e < V; e += kF) {
           Piece<float, kF>::put(part + gc + n * stride + e, aw, n * V + e);
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(kBlock ? kMaxThreads : 256) __maxnreg__(backwa
       }
     return;
   }
-  const int width = A.gper * A.lanes * NV * V, slot = p.unit / A.gper, col0 = (p.unit % A.gper) * A.lanes * NV * V;
+  const int width = A.gper * A.lanes * NV * V, col0 = (p.unit % A.gper) * A.lanes * NV * V;
   if (slot < A.slots) {
 #pragma unroll
     for (int n = 0; n < NV; ++n)
