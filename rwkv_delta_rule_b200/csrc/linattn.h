@@ -19,6 +19,7 @@ template <typename TIn> struct Pass {
   float *ws;             // nseg > 1: [B, H, nseg, 64, 64], slot z is the state that segment z begins with
                          // (joined), or what the segment before it adds to the state
   int reverse;
+  int terms;             // on the tensor cores, bf16 terms of v that the state is summed from: 2, or 3 where it is an output
 };
 // Passes over operands of one shape that run side by side (the backward has three).
 template <typename TIn> struct Passes {

@@ -107,7 +107,7 @@ rwkv7_status prefill(int B, int T, long long total_T, long long max_T, int H, in
   if (st != RWKV7_OK) return st;
   const bool chunk = use_chunk<TIn>(max_T) && total_T > 0;
   const lin::Shape s = shape(w, cu, B, T, total_T, max_T, H, ws_bytes, 1, chunk);
-  const lin::Passes<TIn> p{{{r, k, v, y, s_in, s_out, 0, 0, static_cast<float *>(ws), 0}}, 1, 0};
+  const lin::Passes<TIn> p{{{r, k, v, y, s_in, s_out, 0, 0, static_cast<float *>(ws), 0, 3}}, 1, 0};
   return from_cuda(run_passes(p, s, B, chunk, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -219,9 +219,9 @@ rwkv7_status rwkv7_linattn_backward_bf16(int B, int T, int H, int N, const uint1
   const lin::Shape s = shape(w, nullptr, B, T, tokens, T, H, workspace_bytes, 3, chunk);
   float *ws = static_cast<float *>(workspace);
   const long long part = s.nseg > 1 ? static_cast<long long>(B) * H * s.nseg * kN * kN : 0;
-  const lin::Passes<uint16_t> p{{{dy, v, k, dr, s_in, nullptr, 1, 0, ws, 0},
-                                 {v, dy, r, dk, ds_out, nullptr, 1, 0, ws + part, 1},
-                                 {k, r, dy, dv, ds_out, ds_in, 0, 0, ws + 2 * part, 1}},
+  const lin::Passes<uint16_t> p{{{dy, v, k, dr, s_in, nullptr, 1, 0, ws, 0, 2},
+                                 {v, dy, r, dk, ds_out, nullptr, 1, 0, ws + part, 1, 2},
+                                 {k, r, dy, dv, ds_out, ds_in, 0, 0, ws + 2 * part, 1, 3}},
                                 3, 0};
   if (ds_in != nullptr && (ds_in == ds_out || ds_in == s_in) && s.nseg == 1) {
     // in place, and no workspace that holds the state meanwhile: the pass that writes it goes last

@@ -26,8 +26,9 @@
 //   columns that let MMA3 run beside P (B4 T16384 H64: 685 us with it, 625 without);
 //   w^(L-1-s) v_s in MMA3: three terms, 2^-24 at most, because these sums are the state: with two terms
 //   they would be 2.7e-6 off on average, the three leave 4e-7 (float32 sums of products alone: 2e-7).
-//   Where no state leaves the pass (dr and dk) two, 2^-16 at most: the outputs are bf16, and S0's 2^-8 is
-//   larger (backward B8 T1024 H12 39 us with three there, 34 with two; B2 T4001 H64 220 and 190).
+//   Where the state is no output (dr and dk) two, 2^-16 at most: the outputs are bf16, and S0's 2^-8 is
+//   larger (backward B8 T1024 H12 39 us with three there, 34 with two; B2 T4001 H64 220 and 190).  dv's pass
+//   has three whether or not its state, ds_in, is asked for, so that dv does not depend on that.
 // k, q and v enter their products as they are, exactly.
 //
 // Measured on B200: B4 T16384 H64 (2.15 GB) 431 us, 500 to 535 us back to back, where the card's power
@@ -193,7 +194,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
   // i0 + 8 u, columns j0 + 8 n, + 1
   const int i0 = 16 * rb + (lane >> 2), j0 = 32 * half + 2 * (lane & 3);
   const uint32_t at_s = sm + OFF_S + i0 * 128u + 4 * (lane & 3) + (((4 * half) ^ (lane >> 2)) << 4);
-  const int terms = kOut && A.s_out == nullptr ? 2 : 3;  // of w^(L-1-s) v_s in MMA3, the second of two rounded
+  const int terms = kOut ? A.terms : 3;  // of w^(L-1-s) v_s in MMA3, the second of two rounded
   f32x2 S[8];
   auto put_state = [&]() {  // S in bf16, rows of MMA1's B operand
 #pragma unroll
