@@ -194,7 +194,9 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
   // i0 + 8 u, columns j0 + 8 n, + 1
   const int i0 = 16 * rb + (lane >> 2), j0 = 32 * half + 2 * (lane & 3);
   const uint32_t at_s = sm + OFF_S + i0 * 128u + 4 * (lane & 3) + (((4 * half) ^ (lane >> 2)) << 4);
-  const int terms = kOut ? A.terms : 3;  // of w^(L-1-s) v_s in MMA3, the second of two rounded
+  // of w^(L-1-s) v_s in MMA3, the second of two rounded (a choice of two constants: taken as a number, the backward of
+  // B2 T4001 H64 took 227 us, 193 so)
+  const int terms = kOut && A.terms == 2 ? 2 : 3;
   f32x2 S[8];
   auto put_state = [&]() {  // S in bf16, rows of MMA1's B operand
 #pragma unroll
