@@ -386,7 +386,9 @@ RWKV7_API rwkv7_status rwkv7_wkv_backward_bf16(int B, int T, int H, int N, const
  * bfloat16 calls of 32 tokens and more run in chunks of 128 tokens on the tensor cores: y is then off by
  * its own rounding and by one bf16 rounding each of the products r_t . k_s and of the state a chunk begins
  * with; the states keep float32 accuracy.  A NaN or an infinity among a sequence's operands reaches
- * its later outputs, and there those of up to 127 tokens before it too; it never reaches another sequence.
+ * the results that the recurrence says, where an infinity may arrive as NaN, and no others: of a prefill the outputs
+ * of its token and of later ones (so what stands behind a row's last token in a padded batch spoils none that
+ * counts, only s_out), in dk and dv those of its token and of earlier ones.  It never reaches another sequence.
  *
  * varlen: cu_seqlens and max_T as for rwkv7_wkv_prefill_varlen_bf16.
  * backward: gradients of a loss with dL/dy = dy and dL/ds_out = ds_out (NULL: zero).  It needs the

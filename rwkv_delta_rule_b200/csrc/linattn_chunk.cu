@@ -31,6 +31,14 @@
 //   has three whether or not its state, ds_in, is asked for, so that dv does not depend on that.
 // k, q and v enter their products as they are, exactly.
 //
+// NaN and infinity: zero times them is NaN, so a bad k or v would also spoil the rows of its chunk before it (reversed:
+// behind it).  Such a chunk shows in MMA3's result, whose row (v) or column (k) is not finite then, and its out is
+// formed again by redo_out.  Looking for it there takes 8 operations per thread and chunk and costs nothing that
+// can be measured; selects in P and a sum over the pieces of v instead cost 3 to 5 % of a prefill.
+//
+// Code size counts: both directions of the backward run on an SM at once.  With the polling of a wait unrolled
+// by the compiler and a descriptor formed per MMA, 10 KB more in all, B2 T4001 H64 takes 221 us and 196 as it is.
+//
 // Measured on B200: B4 T16384 H64 (2.15 GB) 431 us, 500 to 535 us back to back, where the card's power
 // limit takes the clock from 1.97 to 1.55 GHz; 296 chains (2 per SM) of 8192 tokens 5.4 TB/s, 83 % of
 // measured HBM.  A chunk takes 2.5 us alone on an SM and 3.6 us with another CTA: no unit is full (issue
@@ -64,9 +72,13 @@ constexpr uint32_t OFF_V = OFF_S + kN * kN * 2, OFF_V1 = OFF_V + kTile, OFF_V2 =
 constexpr uint32_t OFF_PW = OFF_V3 + kTile;  // float [132]: w^n for n <= 128
 constexpr uint32_t OFF_PL = OFF_PW + 528;    // float [132]: what the rounding of w^n to float32 leaves
 constexpr uint32_t OFF_BAR = OFF_PL + 528;   // mbarriers, TMEM address, flags
-constexpr uint32_t kSmemBytes = OFF_BAR + 128 + 1024;
-// Tiles landed (Q and K; V); all warps ready for MMA1, MMA3, MMA2; each of those done; V1's tile free again.
-enum { B_QK, B_V, B_READY, B_SPLIT, B_P, B_M1, B_M3, B_M2, B_OUT, kBars };
+constexpr uint32_t OFF_EDGE = OFF_BAR + 128;  // unsigned [64]: see redo_out
+constexpr uint32_t kSmemBytes = OFF_EDGE + 256 + 1024;
+// Tiles landed (Q and K; V); all warps ready for MMA1, MMA3, MMA2; each of those done; V1's tile free again; a product
+// of redo_out done (two phases per call).
+enum { B_QK, B_V, B_READY, B_SPLIT, B_P, B_M1, B_M3, B_M2, B_OUT, B_REDO, kBars };
+constexpr uint32_t OFF_SLOT = OFF_BAR + 8 * kBars;  // words: TMEM address, bad, stop, redo
+static_assert(OFF_SLOT % 8 == 0 && 8 * kBars + 16 <= 128, "stop and redo are read together");
 
 struct Maps {
   CUtensorMap q, k, v, out;  // [tokens, H, 64] bf16, box {64, 1, 128}
@@ -128,6 +140,142 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, uint32_t sr
                : "memory");
 }
 
+// P in bf16 from 32 columns of products q k: a block on the diagonal, w^(t-s), zero past it: 1 on it, then a factor w
+// per column ...
+template <bool kRev> __device__ __forceinline__ void diagonal_p(float (&v)[32], float (&pk)[16], int lane, float w1) {
+  float f = 0.f;
+#pragma unroll
+  for (int x = 0; x < 32; ++x) {
+    const int e = kRev ? x : 31 - x;
+    f = e == lane ? 1.f : f * w1;
+    v[e] *= f;
+  }
+#pragma unroll
+  for (int x = 0; x < 16; ++x) pk[x] = __uint_as_float(pack2(make2(v[2 * x], v[2 * x + 1])));
+}
+// ... and one off it, w^(t-s) = w^(t - 32 g - 31) w^(31 - x), reversed w^(s-t) = w^(32 g - t) w^x; a is the first factor
+template <bool kRev>
+__device__ __forceinline__ void full_p(const float (&v)[32], float (&pk)[16], float a, float w1, f32x2 w2) {
+  f32x2 f = kRev ? make2(a, a * w1) : make2(a * w1, a);
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    const int e = kRev ? x : 15 - x;
+    pk[e] = __uint_as_float(pack2(mul2(make2(v[2 * e], v[2 * e + 1]), f)));
+    f = mul2(f, w2);
+  }
+}
+
+// The rows of out again, for a chunk with a k or v that is not finite: P with nothing past its diagonal, a bad v as zero
+// in P V and then NaN from its own row on (reversed: up to it).  All other results keep their bits.  Called by the whole
+// CTA behind the chunk's last barrier, when the tiles of V1 to V3 and the first 128 TMEM columns are free and q S0 still
+// is in TMEM; q, k, v, out: the chunk's first row of this head.  edge[channel] = number << 8 | kChunk - n says that
+// from the n-th row on (reversed: counted from the last) the channel is NaN in the CTA's chunk `number`, counted from
+// 1; later chunks' words are larger, so none has to be cleared.  Not inlined: the loop's code has to stay small.
+template <bool kRev>
+__device__ __noinline__ void redo_out(uint32_t sm, uint32_t tmem, const uint16_t *q, const uint16_t *k, const uint16_t *v,
+                                      uint16_t *out, int H, int L, int number) {
+  constexpr int kLead = kRev ? 3 : 4;
+  uint8_t *smem = static_cast<uint8_t *>(__cvta_shared_to_generic(sm));
+  unsigned *edge = reinterpret_cast<unsigned *>(smem + OFF_EDGE);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + OFF_BAR) + B_REDO;
+  volatile int *bad = reinterpret_cast<volatile int *>(smem + OFF_SLOT + 4);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, rb = warp & 3, half = warp >> 2;
+  const int row = 32 * rb + lane, nth = kRev ? kChunk - 1 - row : row;
+  const bool elected = elect_one();
+  const uint32_t at = sm + row * 128u + (((4 * half) ^ (row & 7)) << 4), tml = tmem + (static_cast<uint32_t>(rb) << 21);
+  const long long mine = row * (static_cast<long long>(H) * kN) + 32 * half;
+#pragma unroll 1
+  for (int x = 0; x < 4; ++x) {
+    uint4 u[3] = {};
+    if (row < L) {
+      u[0] = *reinterpret_cast<const uint4 *>(q + mine + 8 * x);
+      u[1] = *reinterpret_cast<const uint4 *>(k + mine + 8 * x);
+      u[2] = *reinterpret_cast<const uint4 *>(v + mine + 8 * x);
+    }
+    uint32_t w[4] = {u[2].x, u[2].y, u[2].z, u[2].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t ones = e & 1 ? 0x7f800000u : 0x7f80u;
+      if ((w[e >> 1] & ones) == ones) {
+        w[e >> 1] &= e & 1 ? 0xffffu : 0xffff0000u;
+        atomicMax(edge + 32 * half + 8 * x + e, static_cast<unsigned>(number) << 8 | static_cast<unsigned>(kChunk - nth));
+      }
+    }
+    const uint32_t wq[4] = {u[0].x, u[0].y, u[0].z, u[0].w}, wk[4] = {u[1].x, u[1].y, u[1].z, u[1].w};
+    sts128((at ^ (16 * x)) + OFF_V1, wq);
+    sts128((at ^ (16 * x)) + OFF_V2, wk);
+    sts128((at ^ (16 * x)) + OFF_V3, w);
+  }
+  // a product issued by the leading warp, which all wait for
+  auto product = [&](int phase, auto issue) {
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
+    named_sync(1, kThreads);
+    tc::tc_fence_after();
+    if (warp == kLead && elected) {
+      issue();
+      tc::mma_commit(bar);
+      if (!tc::mbar_wait_bounded(bar, phase, kMaxPolls)) *bad = 1;
+    }
+    __syncwarp();
+    if (!tc::mbar_wait_bounded(bar, phase, kMaxPolls)) *bad = 1;
+    tc::tc_fence_after();
+  };
+  product(0, [&]() {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+      tc::mma_ss(0, tmem + TM_P, tc::smem_desc(sm + OFF_V1 + ks * 32, 16, 1024),
+                 tc::smem_desc(sm + OFF_V2 + ks * 32, 16, 1024), tc::instr_desc(tc::kFmtBF16, 128, 128, false, false), ks > 0);
+  });
+  const float w1 = lds32(sm + OFF_PW + 4);
+#pragma unroll 1
+  for (int n = 0; n < 2; ++n) {
+    const int g = half + 2 * n;
+    float p[32], pk[16] = {};
+    tc::tmem_ld32(tml + TM_P + 32 * g, p);
+    if (g == rb) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (kRev ? e < lane : e > lane) p[e] = 0.f;
+      diagonal_p<kRev>(p, pk, lane, w1);
+    } else if (kRev ? g > rb : g < rb) {
+      full_p<kRev>(p, pk, lds32(sm + OFF_PW + 4 * (kRev ? 32 * g - row : row - 32 * g - 31)), w1, make2(w1 * w1, w1 * w1));
+    }
+    tc::tmem_st16(tml + TM_P + 32 * half + 16 * n, pk);
+  }
+  tc::tmem_st_wait();
+  product(1, [&]() {
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+      tc::mma_ts_bf16(tmem + TM_Y, tmem + TM_P + 32 * ((ks >> 1) & 1) + 16 * (ks >> 2) + 8 * (ks & 1),
+                      tc::smem_desc(sm + OFF_V3 + ks * 2048, kTile, 1024),
+                      tc::instr_desc(tc::kFmtBF16, 128, 64, false, true), ks > 0);
+  });
+  const float f1 = lds32(sm + OFF_PW + 4 * (kRev ? max(L - 1 - row, 0) : row + 1));
+  float y[32], p[32];
+  tc::tmem_ld32(tml + TM_YS + 32 * half, y);
+  tc::tmem_ld32(tml + TM_Y + 32 * half, p);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    uint32_t u[4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const unsigned c = edge[32 * half + 8 * x + e];
+      if (c >> 8 == static_cast<unsigned>(number) && nth >= kChunk - static_cast<int>(c & 255u))
+        p[8 * x + e] = __int_as_float(0x7fffffff);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      u[e] = pack2(fma2(make2(y[8 * x + 2 * e], y[8 * x + 2 * e + 1]), make2(f1, f1),
+                        make2(p[8 * x + 2 * e], p[8 * x + 2 * e + 1])));
+    sts128((at ^ (16 * x)) + OFF_V1, u);
+    if (L < kChunk && row < L) *reinterpret_cast<uint4 *>(out + mine + 8 * x) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  tc::fence_proxy_async_smem();
+  tc::tc_fence_before();
+  named_sync(1, kThreads);
+}
+
 // One segment of one pass.
 template <bool kRev, bool kOut>
 __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, const Shape &P, int b, int z,
@@ -143,9 +291,10 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
   const long long pair = static_cast<long long>(b) * P.H + h;
 
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + OFF_BAR);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_BAR + 8 * kBars);
-  volatile int *bad = reinterpret_cast<volatile int *>(smem + OFF_BAR + 8 * kBars + 4);  // a wait ran out
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + OFF_SLOT);
+  volatile int *bad = reinterpret_cast<volatile int *>(smem + OFF_SLOT + 4);  // a wait ran out
   volatile int *stop = bad + 1;  // tid 0's copy of it, which all warps act on together
+  volatile int *redo = bad + 2;  // the last chunk, counted from 1, with a k or v that is not finite
 
   const int nchunks = (sg.len + kChunk - 1) / kChunk;
   auto chunk_at = [&](int i) { return kRev ? nchunks - 1 - i : i; };
@@ -166,6 +315,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
       tc::fence_mbar_init();
       *bad = 0;
       *stop = 0;
+      *redo = 0;
       if (nchunks > 0) {
         load(&maps.k, OFF_K, B_QK, 0);
         load(&maps.v, OFF_V, B_V, 0);
@@ -188,6 +338,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
 
   const int rb = warp & 3, half = warp >> 2;  // row block and column half of this warp
   const int row = 32 * rb + lane;
+  if (kOut && tid < kN) *reinterpret_cast<unsigned *>(smem + OFF_EDGE + 4 * tid) = 0u;
   // chunk x of this thread's half row of a swizzled tile is at tile + (at ^ 16 x)
   const uint32_t at = sm + row * 128u + (((4 * half) ^ (row & 7)) << 4);
   // this thread's part of the state, as MMA3's result is read: pair 2 n + u is row (value channel)
@@ -240,6 +391,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
   // return at once: the warps finish their chunk (on whatever is there, within bounds), so that every
   // named barrier is reached by all, and stop together at its end.
   auto wait = [&](int k, int n) -> bool {
+#pragma unroll 1
     for (uint32_t p = 0; p < kMaxPolls; ++p) {
       if (tc::mbar_try_wait(bars + k, n & 1)) return true;
       if ((p & 63u) == 63u && *bad) return false;
@@ -279,10 +431,12 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
         if (wait(B_QK, it) && wait(B_READY, it) && elected) {
           tc::tc_fence_after();
           constexpr uint32_t d1 = tc::instr_desc(tc::kFmtBF16, 128, 192, false, false);
+          // (offsets within a tile are added to a descriptor's address field, 16 bytes a step: shared memory ends below
+          // 2^18, so that nothing carries out of it)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            tc::mma_ss(0, tmem + TM_P, tc::smem_desc(sm + tile_q + ks * 32, 16, 1024),
-                       tc::smem_desc(sm + OFF_K + ks * 32, 16, 1024), d1, ks > 0);
+            tc::mma_ss(0, tmem + TM_P, tc::smem_desc(sm + tile_q, 16, 1024) + ks * 2,
+                       tc::smem_desc(sm + OFF_K, 16, 1024) + ks * 2, d1, ks > 0);
           tc::mma_commit(bars + B_M1);
           ++begun[B_M1];
         }
@@ -344,8 +498,8 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
         for (int t = 0; t < terms; ++t)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            tc::mma_ss(0, tmem + TM_X, tc::smem_desc(sm + OFF_V1 + t * kTile + ks * 2048, kTile, 1024),
-                       tc::smem_desc(sm + tile_k + ks * 2048, kTile, 1024), d3, t + ks > 0);
+            tc::mma_ss(0, tmem + TM_X, tc::smem_desc(sm + OFF_V1 + t * kTile, kTile, 1024) + ks * 128,
+                       tc::smem_desc(sm + tile_k, kTile, 1024) + ks * 128, d3, t + ks > 0);
         tc::mma_commit(bars + B_M3);
         ++begun[B_M3];
       }
@@ -370,29 +524,13 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
           const uint32_t to = tml + TM_P + 32 * half + 16 * n;
           float pk[16];
           if (g == rb) {
-            // w^(t-s), zero past the diagonal: 1 on it, then a factor w per column
-            float v[32], f = 0.f;
-            tc::tmem_ld32(tml + TM_P + 32 * g, v);
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const int e = kRev ? x : 31 - x;
-              f = e == lane ? 1.f : f * w1;
-              v[e] *= f;
-            }
-#pragma unroll
-            for (int x = 0; x < 16; ++x) pk[x] = __uint_as_float(pack2(make2(v[2 * x], v[2 * x + 1])));
-          } else if (kRev ? g > rb : g < rb) {
-            // w^(t-s) = w^(t - 32 g - 31) w^(31 - x), reversed w^(s-t) = w^(32 g - t) w^x
             float v[32];
             tc::tmem_ld32(tml + TM_P + 32 * g, v);
-            const float a = lds32(sm + OFF_PW + 4 * (kRev ? 32 * g - row : row - 32 * g - 31));
-            f32x2 f = kRev ? make2(a, a * w1) : make2(a * w1, a);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const int e = kRev ? x : 15 - x;
-              pk[e] = __uint_as_float(pack2(mul2(make2(v[2 * e], v[2 * e + 1]), f)));
-              f = mul2(f, w2);
-            }
+            diagonal_p<kRev>(v, pk, lane, w1);
+          } else if (kRev ? g > rb : g < rb) {
+            float v[32];
+            tc::tmem_ld32(tml + TM_P + 32 * g, v);
+            full_p<kRev>(v, pk, lds32(sm + OFF_PW + 4 * (kRev ? 32 * g - row : row - 32 * g - 31)), w1, w2);
           } else {
 #pragma unroll
             for (int x = 0; x < 16; ++x) pk[x] = 0.f;
@@ -416,7 +554,7 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
             tc::mma_ts_bf16(tmem + TM_Y, tmem + TM_P + 32 * ((ks >> 1) & 1) + 16 * (ks >> 2) + 8 * (ks & 1),
-                            tc::smem_desc(sm + tile_v + ks * 2048, kTile, 1024), d2,
+                            tc::smem_desc(sm + tile_v, kTile, 1024) + ks * 128, d2,
                             ks > 0);
           tc::mma_commit(bars + B_M2);
           ++begun[B_M2];
@@ -439,6 +577,13 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
       const f32x2 f = make2(f1, f1), fl = make2(f2, f2);
 #pragma unroll
       for (int e = 0; e < 8; ++e) S[e] = fma2(S[e], f, fma2(S[e], fl, x[e]));
+      if (kOut) {
+        // a bad v spoils its whole row of x, a bad k its column: this thread's columns in one row, its other row in one
+        float a, b2, c2, d2;
+        split2(add2(add2(x[0], x[2]), add2(x[4], x[6])), a, b2);
+        split2(x[1], c2, d2);
+        if (!(fabsf(a + b2 + c2) <= 3e38f)) *redo = it + 1;
+      }
     }
     if (kOut) {
       put_state();
@@ -476,7 +621,13 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
     tc::tc_fence_before();
     if (tid == 0) *stop = *bad;
     named_sync(1, kThreads);
-    if (*stop) break;
+    int stopped, again;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(stopped), "=r"(again) : "r"(sm + OFF_SLOT + 8) : "memory");
+    if (stopped) break;
+    if (kOut && again == it + 1) {
+      const long long first = ((sg.lo + c * kChunk) * P.H + h) * kN;
+      redo_out<kRev>(sm, tmem, A.q + first, A.k + first, A.v + first, A.out + first, P.H, L, it + 1);
+    }
     if (kOut && L == kChunk && warp == kStore && elected) {
       tma_store_3d(&maps.out, sm + OFF_V1, 0, h, static_cast<int>(sg.lo) + c * kChunk);
       tc::bulk_commit_group();
