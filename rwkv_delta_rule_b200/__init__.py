@@ -412,7 +412,7 @@ def rwkv7_wkv_backward_bf16(r, w, k, v, a, b, states, dy, ds_out, dr, dw, dk, dv
 
 def _fits(t, name: str, dtype, shape, device) -> int:
     """The address of ``t``, which has to be a contiguous tensor of this type and shape on ``device``."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device.index or not t.is_contiguous():
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != device.index or not t.is_contiguous():
         _check(t, name, dtype, shape)
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}: one device is wanted")
     return t.data_ptr()
@@ -423,6 +423,8 @@ def _fits_or_none(t, name: str, dtype, shape, device) -> Optional[int]:
 
 
 def _device_of(t, name: str):
+    if t is None:
+        raise ValueError(f"{name} is required")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.device
@@ -492,6 +494,15 @@ def _dims(t, name: str, layout: str):
     return t.shape
 
 
+def _rows(cu_seqlens) -> int:
+    """The rows of a ragged batch whose offsets ``[B + 1]`` these are."""
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is required")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError(f"cu_seqlens must be [B + 1], got {tuple(cu_seqlens.shape)}")
+    return cu_seqlens.numel() - 1
+
+
 def _linattn_prefill(name, dtype, r, k, v, w, s_in, y, s_out, workspace, stream):
     dev = _device_of(r, "r")
     B, T, H, N = shape = _dims(r, "r", "B, T, H, 64")
@@ -516,9 +527,9 @@ def rwkv7_linattn_prefill_bf16(r, k, v, w, s_in, y, s_out, workspace=None, strea
 def rwkv7_linattn_prefill_varlen_bf16(cu_seqlens, max_T, r, k, v, w, s_in, y, s_out, workspace=None,
                                       stream=None) -> None:
     """Ragged bfloat16 prefill: operands / y ``[total_T,H,64]`` packed, ``cu_seqlens`` int32 ``[B+1]`` on the device."""
+    Bn = _rows(cu_seqlens)
     dev, bf16 = _device_of(r, "r"), torch.bfloat16
     total, H, N = shape = _dims(r, "r", "total_T, H, 64")
-    Bn = cu_seqlens.numel() - 1
     states = (Bn, H, N, N)
     _call_on(dev, stream, "rwkv7_linattn_prefill_varlen_bf16", Bn, total, int(max_T), H, N,
              _fits(cu_seqlens, "cu_seqlens", torch.int32, (Bn + 1,), dev), _fits(r, "r", bf16, shape, dev),
@@ -732,12 +743,12 @@ def linattn_prefill(r, k, v, w, s_in=None, *, stream=None):
 def linattn_prefill_varlen(cu_seqlens, max_T, r, k, v, w, s_in=None, *, stream=None):
     """Allocate ``y`` and ``s_out`` and run the ragged linear-attention prefill; returns ``(y, s_out)``.
     Tokens of ``y`` that no row owns are left unset."""
-    total, H, N = r.shape
-    B = cu_seqlens.numel() - 1
-    with _on(stream, r.device):
+    B, dev = _rows(cu_seqlens), _device_of(r, "r")
+    _, H, N = _dims(r, "r", "total_T, H, 64")
+    with _on(stream, dev):
         y = torch.empty_like(r)
-        s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
-        ws = _workspace(rwkv7_linattn_workspace(B, max_T, H), r.device)
+        s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=dev)
+        ws = _workspace(rwkv7_linattn_workspace(B, max_T, H), dev)
     rwkv7_linattn_prefill_varlen_bf16(cu_seqlens, max_T, r, k, v, w, s_in, y, s_out, ws, stream)
     return y, s_out
 
@@ -745,9 +756,9 @@ def linattn_prefill_varlen(cu_seqlens, max_T, r, k, v, w, s_in=None, *, stream=N
 def linattn_decode_(r, k, v, w, state, y=None, *, stream=None):
     """One linear-attention step updating ``state`` in place; returns ``y``."""
     if y is None:
-        with _on(stream, r.device):
+        with _on(stream, _device_of(r, "r")):
             y = torch.empty_like(r)
-    f = rwkv7_linattn_decode if r.dtype is torch.float32 else rwkv7_linattn_decode_bf16
+    f = rwkv7_linattn_decode if r is not None and r.dtype is torch.float32 else rwkv7_linattn_decode_bf16
     f(r, k, v, w, state, y, stream)
     return y
 
