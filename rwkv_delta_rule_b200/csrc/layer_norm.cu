@@ -572,9 +572,18 @@ Plan make_plan(size_t elem, int M, int G, int D, bool backward) {
     P.loop = P.threads > kMaxThreads;
   }
   P.gblocks = ceil_div(G, P.gper);
+  if (P.loop) {
+    // the backward's column sums: tiles of 256 columns, and row blocks for 8 rounds of 8 CTAs per SM, so that the last
+    // round counts little.  Each row block is a partial sum: 296 of them whatever the width would be 40 GB for 300
+    // rows of 2^24.  Measured (us; 296 row blocks / 1, 4, 8 rounds), bf16: 4096 x 16384 357 / 400, 331, 339;
+    // 8192 x 12288 518 / 613, 524, 516; 300 x 16384 61 / 35, 42, 46.
+    const int want = ceil_div(8LL * 8 * kSMs, ceil_div(static_cast<long long>(G) * D, 256));
+    P.mblocks = M < want ? M : want;
+    return P;
+  }
   const int rowblocks = ceil_div(M, P.slots);  // CTAs that would take one row per unit
   const int regs = backward ? backward_regs(P.v * P.nv) : forward_regs(P.v * P.nv);
-  const int resident = P.loop ? 2 : 65536 / regs / P.threads;
+  const int resident = 65536 / regs / P.threads;
   const int want = ceil_div(static_cast<long long>(kSMs) * (resident > 0 ? resident : 1), P.gblocks);
   P.mblocks = rowblocks < want ? rowblocks : want;
   return P;
