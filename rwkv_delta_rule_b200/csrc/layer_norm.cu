@@ -204,6 +204,7 @@ __device__ __forceinline__ void fetch(const T *row, bool on, int stride, int lef
 // are read again from L1) and the value per element, and one or two rows fetched ahead: with rows of
 // 8 KB, 48 KB are in flight per SM.  Backward: the weight, two sums, and the row under way and the next of
 // two tensors (24 elements per lane spilled: 32768 x 768 took 73 us with one warp per row, 39 with three).
+// At these limits the kernels with 16 elements, and those with 8 in pieces of one, spill 4 to 76 bytes a thread.
 constexpr int forward_regs(int E) { return E <= 8 ? 64 : E <= 16 ? 80 : 128; }
 constexpr int backward_regs(int E) { return E <= 8 ? 80 : 128; }
 constexpr int kMaxThreads = 512;
@@ -616,12 +617,9 @@ cudaError_t launch_planned(const Plan &P, const Args<T> &A, bool backward, cudaS
   if (!backward) return launch(layer_norm_kernel<T, V, NV, kBlock>, grid, P.threads, 0, stream, A);
   if constexpr (V * NV > 16) return cudaErrorInvalidValue;  // no plan asks for it
   size_t smem = 0;
+  // at most 256 lanes of 16 elements, 32 KB: below what a launch has without asking
   if (!kBlock && P.slots > 1) smem = sizeof(float) * 2 * P.slots * P.gper * P.lanes * P.nv * P.v;
   auto kern = layer_norm_backward_kernel<T, V, (V * NV > 16 ? 1 : NV), kBlock>;
-  if (smem > 48 * 1024 - 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
   return launch(kern, grid, P.threads, smem, stream, A);
 }
 
