@@ -204,7 +204,7 @@ __device__ __forceinline__ void fetch(const T *row, bool on, int stride, int lef
 // are read again from L1) and the value per element, and one or two rows fetched ahead: with rows of
 // 8 KB, 48 KB are in flight per SM.  Backward: the weight, two sums, and the row under way and the next of
 // two tensors (24 elements per lane spilled: 32768 x 768 took 73 us with one warp per row, 39 with three).
-// At these limits the kernels with 16 elements, and those with 8 in pieces of one, spill 4 to 76 bytes a thread.
+// At these limits several kernels with 8 and 16 elements spill, 4 to 76 bytes a thread.
 constexpr int forward_regs(int E) { return E <= 8 ? 64 : E <= 16 ? 80 : 128; }
 constexpr int backward_regs(int E) { return E <= 8 ? 80 : 128; }
 constexpr int kMaxThreads = 512;

@@ -9,7 +9,8 @@
 // and reversed (S <- S + v k^T, out = S q, S <- w S, tokens from the last)
 //     P_ts  = (q_t . k_s) w^(s-t)  for s >= t;   out_t = w^(L-1-t) S0 q_t + ...;
 //     S_0   = w^L S0 + sum_s (w^(s+1) v_s) k_s^T.
-// Only powers w^0 .. w^128 of the head's decay appear, all <= 1, so every w in [0, 1] is exact.
+// Only powers of the head's decay appear, w^0 .. w^128 and, where segments are joined, those of their lengths; all
+// <= 1, so every w in [0, 1] is exact.  Those that scale the state are applied in two float32 terms.
 //
 // One CTA of eight warps walks the chunks of one (b, h) (or of one segment of it), two CTAs per SM: 106 KB of
 // shared memory and 256 TMEM columns each, and what one waits for overlaps the other's work.  Warp w has
@@ -367,15 +368,15 @@ __device__ __forceinline__ void walk(const Maps &maps, const Pass<uint16_t> &A, 
                                      from[state_at(t, i0 + 8 * (e & 1), j0 + 8 * (e >> 1) + 1)]);
     if (kOut && !joined && P.nseg > 1) {
       const double wd = P.w[h];
-      const float wl = static_cast<float>(powi(wd, P.seg_len));
+      const Power wl = power(wd, P.seg_len);
       const int steps = kRev ? sg.n - 1 - z : z;
       for (int s = 1; s <= steps; ++s) {
         const float *u = A.ws + (pair * P.nseg + (kRev ? sg.n - 1 - s : s)) * (kN * kN);
-        const float f = kRev && s == 1 ? static_cast<float>(powi(wd, sg.last_len)) : wl;
+        const Power f = kRev && s == 1 ? power(wd, sg.last_len) : wl;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float2 x = *reinterpret_cast<const float2 *>(u + (i0 + 8 * (e & 1)) * kN + j0 + 8 * (e >> 1));
-          S[e] = fma2(S[e], make2(f, f), make2(x.x, x.y));
+          S[e] = fma2(S[e], make2(f.hi, f.hi), fma2(S[e], make2(f.lo, f.lo), make2(x.x, x.y)));
         }
       }
     }

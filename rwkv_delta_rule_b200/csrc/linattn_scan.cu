@@ -57,8 +57,19 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
   if (!kOut && (kRev ? sg.first : sg.last)) return;
   const long long pair = static_cast<long long>(b) * P.H + h;
   const int tid = threadIdx.x, q = tid & 7, row0 = 4 * (tid >> 3);
-  const float w = P.w[h], wp[5] = {1.f, w, w * w, w * w * w, (w * w) * (w * w)};  // powers, for 4 tokens at once
+  const float w = P.w[h];
   const f32x2 w2 = make2(w, w);
+  // states alone: powers, for 4 tokens at once, and what the rounding of w^4 takes from the state with each four, as a
+  // part of it
+  float wp[5] = {1.f, w, 0.f, 0.f, 0.f}, lost = 0.f;
+  if (!kOut) {
+    const double wd = w;
+    wp[2] = static_cast<float>(wd * wd);
+    wp[3] = static_cast<float>(wd * wd * wd);
+    const Power p4 = power(wd, 4);
+    wp[4] = p4.hi;
+    lost = p4.hi > 1e-30f ? p4.lo / p4.hi : 0.f;
+  }
 
   f32x2 s[4][4];  // columns in pairs
   const float *from = !kOut ? nullptr : P.nseg > 1 ? A.ws + (pair * P.nseg + z) * (kN * kN) : A.s_in + pair * (kN * kN);
@@ -168,6 +179,15 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
     };
     int u = 0;
     for (; u + 4 <= ntok; u += 4) group(u, Count<4>());
+    if (!kOut) {
+      // (its own tokens get up to a rounding too much of it, once)
+      const float l = lost * static_cast<float>(u >> 2);
+      const f32x2 l2 = make2(l, l);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[m][e] = fma2(s[m][e], l2, s[m][e]);
+    }
     for (; u < ntok; ++u) group(u, Count<1>());
     __syncthreads();
     if (kOut) {
@@ -226,7 +246,7 @@ template <typename TIn> __global__ void __launch_bounds__(256) linattn_join_kern
   const long long pair = static_cast<long long>(b) * P.H + h;
   const int e4 = (blockIdx.z & 3) * 256 + threadIdx.x, row = e4 >> 4, col = 4 * (e4 & 15);
   const double w = P.w[h];
-  const float wl = static_cast<float>(powi(w, P.seg_len));
+  const Power wl = power(w, P.seg_len);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (A.s_in != nullptr) {
     const float *f = A.s_in + pair * (kN * kN);
@@ -248,9 +268,9 @@ template <typename TIn> __global__ void __launch_bounds__(256) linattn_join_kern
     for (int j = 0; j < 8; ++j)
       if (i0 + j < n) {
         // the decay over the segment before; the sequence's last one may be of another length
-        float f = wl;
-        if (A.reverse && i0 + j == 1) f = static_cast<float>(powi(w, sg.last_len));
-        s = make_float4(fmaf(s.x, f, u[j].x), fmaf(s.y, f, u[j].y), fmaf(s.z, f, u[j].z), fmaf(s.w, f, u[j].w));
+        const Power f = A.reverse && i0 + j == 1 ? power(w, sg.last_len) : wl;
+        s = make_float4(fmaf(s.x, f.hi, fmaf(s.x, f.lo, u[j].x)), fmaf(s.y, f.hi, fmaf(s.y, f.lo, u[j].y)),
+                        fmaf(s.z, f.hi, fmaf(s.z, f.lo, u[j].z)), fmaf(s.w, f.hi, fmaf(s.w, f.lo, u[j].w)));
         *slot(i0 + j) = s;
       }
   }
