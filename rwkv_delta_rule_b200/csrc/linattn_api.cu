@@ -105,7 +105,8 @@ rwkv7_status prefill(int B, int T, long long total_T, long long max_T, int H, in
                      long long ws_bytes, rwkv7_stream_t stream) {
   const rwkv7_status st = check(B, total_T, H, N, r, k, v, w, s_in, y, s_out, ws, ws_bytes);
   if (st != RWKV7_OK) return st;
-  const bool chunk = use_chunk<TIn>(max_T) && total_T > 0;
+  if (total_T == 0) max_T = 0;
+  const bool chunk = use_chunk<TIn>(max_T);
   const lin::Shape s = shape(w, cu, B, T, total_T, max_T, H, ws_bytes, 1, chunk);
   const lin::Passes<TIn> p{{{r, k, v, y, s_in, s_out, 0, 0, static_cast<float *>(ws), 0, 3}}, 1, 0};
   return from_cuda(run_passes(p, s, B, chunk, reinterpret_cast<cudaStream_t>(stream)));

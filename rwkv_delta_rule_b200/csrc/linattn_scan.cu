@@ -46,15 +46,18 @@ __device__ __forceinline__ void stage(const Pass<TIn> &A, TIn *buf, long long to
   }
 }
 
+// Reversed walks are bf16 (gradients), passes for the states alone float32: bf16 sequences that come here are too short
+// to be split.
 template <typename TIn, bool kRev, bool kOut>
 __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P, int b, int z, uint8_t *smem_raw) {
+  static_assert(sizeof(TIn) == 2 ? kOut : !kRev, "no call asks for it");
   using C = Tile<TIn>;
   TIn *bufs = reinterpret_cast<TIn *>(smem_raw);
   float *ys = reinterpret_cast<float *>(smem_raw + 2 * C::kElems * sizeof(TIn));
   const int h = blockIdx.x;
   const Segment sg = segment(P, b, z);
   if (sg.len < 0) return;
-  if (!kOut && (kRev ? sg.first : sg.last)) return;
+  if (!kOut && sg.last) return;
   const long long pair = static_cast<long long>(b) * P.H + h;
   const int tid = threadIdx.x, q = tid & 7, row0 = 4 * (tid >> 3);
   const float w = P.w[h];
@@ -118,7 +121,7 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           // states alone: all that decays by the group's end is scaled here
-          if (!kOut) v[m] *= wp[kRev ? kG - j : kG - 1 - j];
+          if (!kOut) v[m] *= wp[kG - 1 - j];
           vv[j][m] = make2(v[m], v[m]);
         }
         if (kOut) {
@@ -204,7 +207,7 @@ __device__ __forceinline__ void scan_segment(const Pass<TIn> &A, const Shape &P,
   }
 
   const bool ends = kRev ? sg.first : sg.last;
-  float *to = !kOut ? A.ws + (pair * P.nseg + (kRev ? z - 1 : z + 1)) * (kN * kN) : A.s_out + pair * (kN * kN);
+  float *to = !kOut ? A.ws + (pair * P.nseg + z + 1) * (kN * kN) : A.s_out + pair * (kN * kN);
   if (!kOut || (ends && A.s_out != nullptr)) {
 #pragma unroll
     for (int m = 0; m < 4; ++m)
@@ -225,11 +228,15 @@ __global__ void __launch_bounds__(kThreads, 7) linattn_scan_kernel(const __grid_
   pdl_wait();
   pdl_trigger();
   const int b = sorted_row(P, blockIdx.y, gridDim.y, lens);
-  const int nz = kOut ? P.nseg : P.nseg - 1, role = blockIdx.z / nz, z = blockIdx.z - role * nz;
-  if (A.p[role].reverse)
-    scan_segment<TIn, true, kOut>(A.p[role], P, b, kOut ? z : z + 1, smem_raw);
-  else
-    scan_segment<TIn, false, kOut>(A.p[role], P, b, z, smem_raw);
+  if constexpr (sizeof(TIn) == 4) {
+    scan_segment<TIn, false, kOut>(A.p[0], P, b, blockIdx.z, smem_raw);
+  } else {
+    const int role = blockIdx.z / P.nseg, z = blockIdx.z - role * P.nseg;
+    if (A.p[role].reverse)
+      scan_segment<TIn, true, kOut>(A.p[role], P, b, z, smem_raw);
+    else
+      scan_segment<TIn, false, kOut>(A.p[role], P, b, z, smem_raw);
+  }
 }
 
 // One thread per 4 columns of a state row, along the segments.
@@ -284,8 +291,11 @@ cudaError_t launch_linattn_scan(const lin::Passes<TIn> &A, const lin::Shape &P, 
   const int nz = A.state_only ? P.nseg - 1 : P.nseg;
   if (nz <= 0) return cudaSuccess;
   const dim3 grid(P.H, B, nz * A.n);
-  return launch_waiting(A.state_only ? linattn_scan_kernel<TIn, false> : linattn_scan_kernel<TIn, true>, grid, kThreads,
-                        Tile<TIn>::kSmem, stream, A, P);
+  if constexpr (sizeof(TIn) == 4) {
+    if (A.state_only)
+      return launch_waiting(linattn_scan_kernel<TIn, false>, grid, kThreads, Tile<TIn>::kSmem, stream, A, P);
+  }
+  return launch_waiting(linattn_scan_kernel<TIn, true>, grid, kThreads, Tile<TIn>::kSmem, stream, A, P);
 }
 
 template <typename TIn>

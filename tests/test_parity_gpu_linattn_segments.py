@@ -53,3 +53,18 @@ def test_segments_keep_the_precision(dtype, B, T, H):
     if dtype == F32:
         off = rel(y.transpose(0, 2), want_y.transpose(0, 2))
         assert bool((off <= tol).all()), ("y", float((off / tol).max()))
+
+
+@pytest.mark.parametrize("max_T", [0, 20, 5000])
+def test_ragged_batch_without_tokens(max_T):
+    """Rows of no tokens at all leave the states as they are, whatever max_T and the workspace would allow."""
+    need_cuda()
+    B, H = 3, 2
+    e = torch.empty(0, H, 64, dtype=BF16, device="cuda")
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    st = torch.randn(B, H, 64, 64, device="cuda")
+    w = torch.full((H,), 0.5, device="cuda")
+    _, s = lib7.linattn_prefill_varlen(cu, max_T, e, e, e, w, st)
+    _, z = lib7.linattn_prefill_varlen(cu, max_T, e, e, e, w)
+    torch.cuda.synchronize()
+    assert torch.equal(s, st) and not bool(z.any())
