@@ -379,8 +379,8 @@ RWKV7_API rwkv7_status rwkv7_wkv_backward_bf16(int B, int T, int H, int N, const
  * workspace: caller-owned device memory (16-byte aligned) in which a prefill or backward splits its
  * sequences into segments that run side by side: rwkv7_linattn_workspace(B, max_T, H) bytes, or
  * rwkv7_linattn_backward_workspace(B, T, H), are the most it uses (0: it does not split).  With fewer
- * bytes it splits less, with NULL and 0 not at all; the results are the same up to float32 rounding
- * order.  The contents need no preparation and mean nothing afterwards; calls that may run at once
+ * bytes it splits less, with NULL and 0 not at all; the states are the same up to float32 rounding order, and
+ * bf16 outputs up to what that changes in the roundings to bf16 named below.  The contents need no preparation and mean nothing afterwards; calls that may run at once
  * need workspaces of their own, replays of a captured call included.
  *
  * bfloat16 calls of 32 tokens and more run in chunks of 128 tokens on the tensor cores: y is then off by

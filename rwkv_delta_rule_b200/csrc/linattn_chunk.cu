@@ -40,7 +40,7 @@
 // Code size counts: both directions of the backward run on an SM at once.  With the polling of a wait unrolled
 // by the compiler and a descriptor formed per MMA, 10 KB more in all, B2 T4001 H64 takes 221 us and 196 as it is.
 //
-// Measured on B200: B4 T16384 H64 (2.15 GB) 431 us, 500 to 535 us back to back, where the card's power
+// Measured on B200: B4 T16384 H64 (2.15 GB) 431 us, 476 to 540 us back to back, where the card's power
 // limit takes the clock from 1.97 to 1.55 GHz; 296 chains (2 per SM) of 8192 tokens 5.4 TB/s, 83 % of
 // measured HBM.  A chunk takes 2.5 us alone on an SM and 3.6 us with another CTA: no unit is full (issue
 // slots 33 %, tensor pipe 40 %, shared memory about half), the chain from barrier to barrier is what is

@@ -7,8 +7,8 @@
 // operations, 5 shared-memory loads and the row sums per thread and token.  These sums meet in a 4-shuffle
 // reduce-scatter over the 8 lanes of a row group.  Operands are staged by cp.async in double-buffered tiles.
 // Measured on B200: float32 B1 T1000 H12 28 us (states, join and outputs in three launches, 42
-// segments of 24 tokens); B8 T4096 H12 422, where tiles twice as long with 4 CTAs per SM took 558, with scalar
-// operations 603.
+// segments of 24 tokens); B8 T4096 H12 418, B4 T8192 H64 1999.  B8 T4096 H12 took 558 with tiles twice as long and 4
+// CTAs per SM, 603 with scalar operations.
 #include "linattn.h"
 #include "packed.cuh"
 
